@@ -17,6 +17,12 @@ CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, "qknorm.cu")]
 HEADERS = [os.path.join(INCLUDE, "qknorm.h")] + sorted(
     os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh"))
+# The 4-bit key/value cache (include/qknorm_kv4.h): a translation unit of its
+# own in the same library.
+KV4_CSRC = os.path.join(CSRC, "kv4")
+KV4_SOURCES = [os.path.join(KV4_CSRC, "kv4.cu")]
+KV4_HEADERS = [os.path.join(INCLUDE, "qknorm_kv4.h")] + sorted(
+    os.path.join(KV4_CSRC, f) for f in os.listdir(KV4_CSRC) if f.endswith(".cuh"))
 LIB_PATH = os.path.join(PKG, "libqknorm.so")
 # The tensor-parallel exchange protocol built for the host (tests only).
 TP_HOST_SOURCE = os.path.join(CSRC, "tp_exchange_host.cc")
@@ -62,8 +68,8 @@ def code_only(text: str) -> str:
 
 
 def kernel_sources() -> list:
-    """The files compiled into the kernels: the translation unit and the
-    headers beside it."""
+    """The files compiled into the QK-Norm kernels: their translation unit and
+    the headers beside it."""
     return sorted(SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                              if f.endswith((".cuh", ".h"))])
 
@@ -87,7 +93,8 @@ def is_stale() -> bool:
     if not os.path.exists(LIB_PATH):
         return True
     t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(p) > t for p in SOURCES + HEADERS)
+    return any(os.path.getmtime(p) > t
+               for p in SOURCES + HEADERS + KV4_SOURCES + KV4_HEADERS)
 
 
 def build(force: bool = False, extra_flags=(), out: str = LIB_PATH) -> str:
@@ -95,7 +102,8 @@ def build(force: bool = False, extra_flags=(), out: str = LIB_PATH) -> str:
     if not force and out == LIB_PATH and not is_stale():
         return out
     tmp = out + ".%d.tmp" % os.getpid()
-    cmd = [nvcc(), *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, *SOURCES, "-o", tmp]
+    cmd = [nvcc(), *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, *SOURCES, *KV4_SOURCES, "-t", "2",
+           "-o", tmp]
     subprocess.check_call(cmd)
     os.replace(tmp, out)
     return out

@@ -1,0 +1,367 @@
+// kv4.cu -- the 4-bit key/value cache (declared in include/qknorm_kv4.h):
+// argument checks, launch shapes and the C entry points.  The library's second
+// translation unit; the kernels are in the headers beside it.
+#include <cuda_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "qknorm_kv4.h"
+
+#include "attention.cuh"
+#include "cache.cuh"
+#include "evict.cuh"
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+thread_local int g_last_error = 0;
+
+int cuda_fail(cudaError_t e)
+{
+    g_last_error = (int)e;
+    return QKN_ERR_CUDA;
+}
+
+// SMs of the current device, looked up once for each.
+std::atomic<int> g_sms[kMaxDevices];
+
+int device_sms(int *sms)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 0 || dev >= kMaxDevices) return QKN_ERR_UNSUPPORTED;
+    int n = g_sms[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return cuda_fail(e);
+        g_sms[dev].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
+    return QKN_OK;
+}
+
+template <typename... Params, typename... Args>
+int launch(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+           Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? QKN_OK : cuda_fail(e);
+}
+
+bool aligned(const void *p, unsigned bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
+
+int elem_size(int dtype)
+{
+    switch (dtype) {
+    case QKN_BF16: return 2;
+    case QKN_FP32: return 4;
+    case QKN_FP16: return 2;
+    case QKN_FP8_E4M3: return 1;
+    default: return 0;
+    }
+}
+
+// Checks of a pool; fills `out` for the kernels.
+int check_pool(const void *pool, int64_t num_pages, int page_size, int Hk, int D, Pool *out)
+{
+    if (D != 64 && D != 128 && D != 256) return QKN_ERR_UNSUPPORTED;
+    if (Hk < 1 || num_pages < 1) return QKN_ERR_SHAPE;
+    int log2_page = 4;
+    while (log2_page < 8 && (1 << log2_page) != page_size) ++log2_page;
+    if ((1 << log2_page) != page_size) return QKN_ERR_SHAPE;
+    const int64_t head = (int64_t)(page_size / kBlockRows) * (16 * D + 128);
+    if (num_pages > INT64_MAX / head / Hk) return QKN_ERR_SHAPE;
+    if (pool == nullptr) return QKN_ERR_NULL;
+    if (!aligned(pool, 16)) return QKN_ERR_ALIGN;
+    out->base = static_cast<uint8_t *>(const_cast<void *>(pool));
+    out->pages = num_pages;
+    out->page_bytes = head * Hk;
+    out->head_bytes = (int)head;
+    out->log2_page = log2_page;
+    out->Hk = Hk;
+    return QKN_OK;
+}
+
+// Rows of `width` elements, `stride` apart.
+int check_rows(int dtype, int64_t rows, int64_t width, int64_t stride)
+{
+    const int es = elem_size(dtype);
+    if (es == 0) return QKN_ERR_UNSUPPORTED;
+    if (rows < 0 || stride < width) return QKN_ERR_SHAPE;
+    if (rows > 0 && stride > 0 && rows > INT64_MAX / stride / es) return QKN_ERR_SHAPE;
+    if (((stride * es) & 15) != 0) return QKN_ERR_ALIGN;
+    return QKN_OK;
+}
+
+template <typename F, typename... Args>
+int by_type(int dtype, int D, Args... args)
+{
+#define QKN_BY_D(TS)                                                                           \
+    switch (D) {                                                                               \
+    case 64: return F::template run<TS, 64>(args...);                                          \
+    case 128: return F::template run<TS, 128>(args...);                                        \
+    default: return F::template run<TS, 256>(args...);                                         \
+    }
+    switch (dtype) {
+    case QKN_BF16: QKN_BY_D(__nv_bfloat16)
+    case QKN_FP32: QKN_BY_D(float)
+    case QKN_FP16: QKN_BY_D(__half)
+    default: QKN_BY_D(__nv_fp8_e4m3)
+    }
+#undef QKN_BY_D
+}
+
+// Blocks for `groups` sub-warps of `lanes` lanes: as many as they fill, at
+// most `per_sm` to an SM.
+int stream_grid(uint64_t groups, int lanes, int per_sm, unsigned *grid)
+{
+    int sms = 0;
+    const int rc = device_sms(&sms);
+    if (rc != QKN_OK) return rc;
+    const uint64_t per_block = kAppendThreads / lanes;
+    const uint64_t want = (groups + per_block - 1) / per_block;
+    const uint64_t cap = (uint64_t)sms * per_sm;
+    *grid = (unsigned)(want < cap ? want : cap);
+    return QKN_OK;
+}
+
+struct Append {
+    template <typename TS, int D>
+    static int run(void *qkv, int64_t T, int Hq, int Hk, int64_t row_stride, const float *gq,
+                   const float *gk, float eps, const int64_t *slots, Pool pool, float *scores,
+                   bool norm, cudaStream_t stream)
+    {
+        constexpr int kNV = D / Storage<TS>::kVec;
+        unsigned grid = 0;
+        const uint64_t rows = (uint64_t)T * (uint64_t)(norm ? Hq + 2 * Hk : 2 * Hk);
+        const int rc = stream_grid(rows, kNV < 32 ? kNV : 32, 6, &grid);
+        if (rc != QKN_OK) return rc;
+        auto kern = norm ? qkn_kv4_append_kernel<TS, D, true> : qkn_kv4_append_kernel<TS, D, false>;
+        return launch(kern, dim3(grid), kAppendThreads, 0, stream, static_cast<TS *>(qkv),
+                      row_stride, T, Hq, Hk, gq, gk, eps, slots, pool, scores);
+    }
+};
+
+struct Read {
+    template <typename TS, int D>
+    static int run(Pool pool, const int64_t *slots, int64_t N, void *k, void *v,
+                   int64_t row_stride, cudaStream_t stream)
+    {
+        constexpr int kNV = D / Storage<TS>::kVec;
+        unsigned grid = 0;
+        const int rc = stream_grid((uint64_t)N * 2 * pool.Hk, kNV < 32 ? kNV : 32, 8, &grid);
+        if (rc != QKN_OK) return rc;
+        return launch(qkn_kv4_read_kernel<TS, D>, dim3(grid), kAppendThreads, 0, stream, pool,
+                      slots, N, static_cast<TS *>(k), static_cast<TS *>(v), row_stride);
+    }
+};
+
+struct Attention {
+    template <typename TS, int D>
+    static int run(AttentionArgs a, cudaStream_t stream)
+    {
+        int rc = launch(qkn_kv4_attention_kernel<TS, D>,
+                        dim3((unsigned)a.B, (unsigned)a.max_q, (unsigned)a.Hq), kSimpleWarps * 32, 0,
+                        stream, a);
+        if (rc != QKN_OK || a.scores == nullptr) return rc;
+        return launch(qkn_kv4_scores_kernel<TS, D>, dim3((unsigned)a.B, (unsigned)a.pool.Hk, 64u),
+                      kSimpleWarps * 32, 0, stream, a);
+    }
+};
+
+int attention_shape(int64_t B, int dtype, int Hq, int Hk, int D, int max_q, int64_t max_kv)
+{
+    if (elem_size(dtype) == 0) return QKN_ERR_UNSUPPORTED;
+    if (D != 64 && D != 128 && D != 256) return QKN_ERR_UNSUPPORTED;
+    if (B < 0 || B > 65535 || Hk < 1 || Hq < 1 || Hq > 65535 || Hq % Hk != 0 || max_q < 1 ||
+        max_q > 65535 || max_kv < 0 || max_kv > INT32_MAX)
+        return QKN_ERR_SHAPE;
+    return QKN_OK;
+}
+
+int64_t attention_workspace(int64_t B, int dtype, int Hq, int Hk, int D, int max_q,
+                            int64_t max_kv, int with_scores)
+{
+    return (int64_t)4 * B * max_q * Hq + 16;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qknorm_kv4_append(void *qkv, int dtype, int64_t T, int Hq, int Hk, int D, int64_t row_stride,
+                      const float *gamma_q, const float *gamma_k, float eps, const int64_t *slots,
+                      void *pool, int64_t num_pages, int page_size, float *scores, void *stream)
+{
+    if (elem_size(dtype) == 0) return QKN_ERR_UNSUPPORTED;
+    if (D != 64 && D != 128 && D != 256) return QKN_ERR_UNSUPPORTED;
+    if (Hq < 0 || Hk < 1 || T < 0) return QKN_ERR_SHAPE;
+    int rc = check_rows(dtype, T, ((int64_t)Hq + 2 * (int64_t)Hk) * D, row_stride);
+    if (rc != QKN_OK) return rc;
+    if (!(eps >= 0.f) || !isfinite(eps)) return QKN_ERR_EPS;
+    if (T == 0) return QKN_OK;
+    Pool p = {};
+    if ((rc = check_pool(pool, num_pages, page_size, Hk, D, &p)) != QKN_OK) return rc;
+    const bool norm = gamma_q != nullptr || gamma_k != nullptr;
+    if (qkv == nullptr || slots == nullptr) return QKN_ERR_NULL;
+    if (norm && (gamma_k == nullptr || (Hq > 0 && gamma_q == nullptr))) return QKN_ERR_NULL;
+    if (!aligned(qkv, 16) || !aligned(slots, 8) || !aligned(gamma_q, 16) || !aligned(gamma_k, 16) ||
+        !aligned(scores, 4))
+        return QKN_ERR_ALIGN;
+    return by_type<Append>(dtype, D, qkv, T, Hq, Hk, row_stride, gamma_q, gamma_k, eps, slots, p,
+                           scores, norm, static_cast<cudaStream_t>(stream));
+}
+
+int qknorm_kv4_read(const void *pool, int64_t num_pages, int page_size, int Hk, int D,
+                    const int64_t *slots, int64_t N, void *k, void *v, int dtype,
+                    int64_t row_stride, void *stream)
+{
+    Pool p = {};
+    int rc = check_pool(pool, num_pages, page_size, Hk, D, &p);
+    if (rc != QKN_OK) return rc;
+    if ((rc = check_rows(dtype, N, (int64_t)Hk * D, row_stride)) != QKN_OK) return rc;
+    if (N == 0) return QKN_OK;
+    if (slots == nullptr || (k == nullptr && v == nullptr)) return QKN_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8)) return QKN_ERR_ALIGN;
+    return by_type<Read>(dtype, D, p, slots, N, k, v, row_stride,
+                         static_cast<cudaStream_t>(stream));
+}
+
+int qknorm_kv4_attention_workspace(int64_t B, int dtype, int Hq, int Hk, int D, int max_q,
+                                   int64_t max_kv, int with_scores, int64_t *bytes)
+{
+    if (bytes == nullptr) return QKN_ERR_NULL;
+    *bytes = 0;
+    const int rc = attention_shape(B, dtype, Hq, Hk, D, max_q, max_kv);
+    if (rc != QKN_OK) return rc;
+    *bytes = attention_workspace(B, dtype, Hq, Hk, D, max_q, max_kv, with_scores);
+    return QKN_OK;
+}
+
+int qknorm_kv4_attention(const void *q, int dtype, int64_t T, int Hq, int Hk, int D,
+                         int64_t row_stride, const void *pool, int64_t num_pages, int page_size,
+                         const int32_t *page_table, int64_t table_stride, int64_t max_pages,
+                         const int32_t *kv_lens, int64_t B, const int32_t *q_starts, int max_q,
+                         float scale, void *out, int64_t out_stride, float *lse, float *scores,
+                         void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (page_size < 16 || page_size > 256 || max_pages < 0 || max_pages > INT32_MAX / page_size)
+        return QKN_ERR_SHAPE;
+    int rc = attention_shape(B, dtype, Hq, Hk, D, max_q, max_pages * page_size);
+    if (rc != QKN_OK) return rc;
+    if ((rc = check_rows(dtype, T, (int64_t)Hq * D, row_stride)) != QKN_OK) return rc;
+    if ((rc = check_rows(dtype, T, (int64_t)Hq * D, out_stride)) != QKN_OK) return rc;
+    if (table_stride < max_pages || T > INT32_MAX) return QKN_ERR_SHAPE;
+    if (q_starts == nullptr && (T != B || max_q != 1)) return QKN_ERR_SHAPE;
+    if (!isfinite(scale)) return QKN_ERR_SHAPE;
+    if (B == 0 || T == 0) return QKN_OK;
+    Pool p = {};
+    if ((rc = check_pool(pool, num_pages, page_size, Hk, D, &p)) != QKN_OK) return rc;
+    if (q == nullptr || (max_pages > 0 && page_table == nullptr) || kv_lens == nullptr ||
+        out == nullptr || workspace == nullptr)
+        return QKN_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) ||
+        !aligned(page_table, 4) || !aligned(kv_lens, 4) || !aligned(q_starts, 4) ||
+        !aligned(lse, 4) || !aligned(scores, 4))
+        return QKN_ERR_ALIGN;
+    if (workspace_bytes <
+        attention_workspace(B, dtype, Hq, Hk, D, max_q, max_pages * page_size, scores != nullptr))
+        return QKN_ERR_SHAPE;
+    AttentionArgs a = {};
+    a.q = q;
+    a.T = T;
+    a.row_stride = row_stride;
+    a.out_stride = out_stride;
+    a.Hq = Hq;
+    a.group = Hq / Hk;
+    a.pool = p;
+    a.page_table = page_table;
+    a.table_stride = table_stride;
+    a.max_pages = max_pages;
+    a.kv_lens = kv_lens;
+    a.B = (int)B;
+    a.q_starts = q_starts;
+    a.max_q = max_q;
+    a.scale = scale;
+    a.out = out;
+    a.lse = lse;
+    a.row_lse = static_cast<float *>(workspace);
+    a.scores = scores;
+    return by_type<Attention>(dtype, D, a, static_cast<cudaStream_t>(stream));
+}
+
+int qknorm_kv4_evict(void *pool, int64_t num_pages, int page_size, int Hk, int D, float *scores,
+                     const int32_t *page_table, int64_t table_stride, int64_t max_pages,
+                     const int32_t *kv_lens, int64_t B, const int32_t *dst_table,
+                     int64_t dst_stride, int64_t dst_pages, int64_t budget, int64_t recent,
+                     int32_t *new_lens, int32_t *kept, void *stream)
+{
+    Pool p = {};
+    if (page_size < 16 || page_size > 256 || max_pages < 0 || max_pages > INT32_MAX / page_size ||
+        dst_pages < 0 || dst_pages > INT32_MAX / page_size)
+        return QKN_ERR_SHAPE;
+    if (B < 0 || table_stride < max_pages || dst_stride < dst_pages || budget < 1 ||
+        budget > dst_pages * page_size || recent < 0 || recent > budget || Hk < 1 ||
+        B > INT32_MAX / Hk)
+        return QKN_ERR_SHAPE;
+    if (B == 0) return QKN_OK;
+    int rc = check_pool(pool, num_pages, page_size, Hk, D, &p);
+    if (rc != QKN_OK) return rc;
+    if (scores == nullptr || (max_pages > 0 && page_table == nullptr) || kv_lens == nullptr ||
+        dst_table == nullptr || new_lens == nullptr || kept == nullptr)
+        return QKN_ERR_NULL;
+    if (!aligned(scores, 4) || !aligned(page_table, 4) || !aligned(kv_lens, 4) ||
+        !aligned(dst_table, 4) || !aligned(new_lens, 4) || !aligned(kept, 4))
+        return QKN_ERR_ALIGN;
+    EvictArgs a = {};
+    a.pool = p;
+    a.scores = scores;
+    a.page_table = page_table;
+    a.table_stride = table_stride;
+    a.max_pages = max_pages;
+    a.kv_lens = kv_lens;
+    a.dst_table = dst_table;
+    a.dst_stride = dst_stride;
+    a.B = B;
+    a.budget = (int)budget;
+    a.recent = (int)recent;
+    a.new_lens = new_lens;
+    a.kept = kept;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    rc = launch(qkn_kv4_select_kernel, dim3((unsigned)(B * Hk)), kSelectThreads, 0, s, a);
+    if (rc != QKN_OK) return rc;
+    unsigned grid = 0;
+    if ((rc = stream_grid((uint64_t)B * Hk * budget, D / 16, 8, &grid)) != QKN_OK) return rc;
+    auto kern = D == 64 ? qkn_kv4_move_kernel<64>
+                        : (D == 128 ? qkn_kv4_move_kernel<128> : qkn_kv4_move_kernel<256>);
+    return launch(kern, dim3(grid), 256, 0, s, a);
+}
+
+int qknorm_kv4_bad_pages(unsigned int *count)
+{
+    if (count == nullptr) return QKN_ERR_NULL;
+    const cudaError_t e = cudaMemcpyFromSymbol(count, g_kv4_bad_pages, sizeof(unsigned int));
+    return e == cudaSuccess ? QKN_OK : cuda_fail(e);
+}
+
+int qknorm_kv4_last_cuda_error(void) { return g_last_error; }
+
+int qknorm_kv4_version(void) { return 100; }
+
+}  // extern "C"

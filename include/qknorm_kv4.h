@@ -1,0 +1,157 @@
+/*
+ * qknorm_kv4.h -- C ABI of libqknorm.so, second part: a paged key/value cache
+ * held in 4 bits, fed by QK-Norm (qknorm.h), with the attention that reads it
+ * and eviction by accumulated attention weight, on NVIDIA B200 (sm_100a).
+ *
+ * The cache.  A pool is `num_pages` pages of `page_size` token slots (16, 32,
+ * 64, 128 or 256) in caller-owned device memory, 16-byte aligned, contiguous:
+ *
+ *     pool[num_pages][Hk][page_size / 16][16 * D + 128]       (bytes)
+ *
+ * One block of 16 slots of one key/value head holds
+ *
+ *     [0, 8*D)             K codes: 16 rows of D/2 bytes
+ *     [8*D, 16*D)          V codes: 16 rows of D/2 bytes
+ *     [16*D, 16*D + 64)    K parameters: 16 pairs of bf16 {scale, mid}
+ *     [16*D + 64, +128)    V parameters: likewise
+ *
+ * Element 2j of a row is the low nibble of its byte j and element 2j+1 the
+ * high one; a code c stands for  mid + scale * (c - 8).  Slot s of the pool
+ * is slot s % page_size of page s / page_size.  `scores`, where a cache has
+ * them, is float[num_pages][Hk][page_size]: each slot's accumulated attention
+ * weight.  A sequence's rows 0, 1, 2, ... lie in the pages its row of the
+ * page table names, page_size to a page.
+ *
+ * How a row y[0..D) is held (fp32 arithmetic, each step rounded to nearest):
+ *     s = (max/2 - min/2) * (2/15), 0 if below 2^-126;   m = min + 8*s
+ *     c_j = clamp(rint((y_j - m) * (1/s)), -8, 7) + 8    (8 when s = 0)
+ *     scale = bf16(s * f), mid = bf16(m * f)
+ * with f = 1 and y the stored row itself, except for keys whose norm
+ * qknorm_kv4_append computes: there y_j = x_j * gamma_k[j] and f is the row's
+ * inverse RMS.  (The codes of a row do not change when the row is multiplied
+ * by a positive number, so the norm's factor goes into the two parameters and
+ * the normalised key is not rounded to the storage type before it is held.)
+ * A row with a NaN or an infinity is held as NaN in every element.
+ *
+ * Common arguments are those of qknorm.h (dtype, D = 64, 128 or 256, 16-byte
+ * alignment of buffers and row strides, `stream`).  Hk >= 1.  The library
+ * allocates nothing and keeps nothing between calls; calls are asynchronous
+ * and stream-ordered, run on the current device, and can be captured in CUDA
+ * graphs.  A workspace is read only where the same call wrote it, so calls
+ * that do not overlap on the GPU may share one.  Entry points return a
+ * qkn_status and launch nothing when they reject an argument; after
+ * QKN_ERR_CUDA, qknorm_kv4_last_cuda_error() gives the cudaError_t.
+ *
+ * Page numbers, slots and lengths are device data that no call can check
+ * before it launches.  The kernels check them instead: a page or slot outside
+ * the pool is never accessed and counts in qknorm_kv4_bad_pages; lengths are
+ * taken into [0, max_pages * page_size], and query ranges into [0, T] and at
+ * most max_q tokens.
+ */
+#ifndef QKNORM_KV4_H
+#define QKNORM_KV4_H
+
+#include <stdint.h>
+
+#include "qknorm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * Store new tokens: per-head QK-Norm of a fused QKV buffer in place (exactly
+ * qknorm_per_head), with its key and value rows also written to the cache, in
+ * one pass over the buffer.  Token t's rows go to slot slots[t] (int64, device,
+ * 8-byte aligned); a negative slot stores nothing (a padded token; its norm is
+ * still done).  With gamma_q and gamma_k both NULL nothing is normalised and
+ * only K and V are read: the buffer was normalised before, layerwise for
+ * instance.  Otherwise gamma_k must be given, and gamma_q unless Hq == 0.
+ * scores may be NULL; else the stored slots' scores become 0.  No slot may
+ * occur twice in one call: which token's bytes it would hold is undefined.
+ */
+int qknorm_kv4_append(void *qkv, int dtype, int64_t T, int Hq, int Hk, int D, int64_t row_stride,
+                      const float *gamma_q, const float *gamma_k, float eps, const int64_t *slots,
+                      void *pool, int64_t num_pages, int page_size, float *scores, void *stream);
+
+/*
+ * Read rows back as values: row i of k and of v (Hk*D elements of `dtype`,
+ * row_stride elements apart) gets what slot slots[i] holds, rounded once (FP8
+ * saturates to +-448).  A slot outside the pool reads as zeros.  k or v may be
+ * NULL, not both.
+ */
+int qknorm_kv4_read(const void *pool, int64_t num_pages, int page_size, int Hk, int D,
+                    const int64_t *slots, int64_t N, void *k, void *v, int dtype,
+                    int64_t row_stride, void *stream);
+
+/*
+ * Attention over the cache.  B sequences; sequence b has kv_lens[b] cached
+ * rows (int32) in the pages page_table[b * table_stride + 0 .. max_pages)
+ * (int32) and the query tokens q_starts[b] .. q_starts[b+1] (int32, B + 1
+ * entries, non-decreasing, at most max_q tokens each) of the fused buffer q
+ * [T, row_stride], whose first Hq*D columns are the query heads.  q_starts
+ * NULL: one token for each sequence, T == B.  Hk must divide Hq; query head h
+ * reads key/value head h / (Hq/Hk).  The last query token of a sequence sees
+ * all of its cached rows and each earlier one a row fewer (the new tokens' own
+ * rows are in the cache, at its end).  For each query token and head
+ *     p = softmax(scale * q . K^T),  out = p V,  lse = log sum exp(scale * q . K^T)
+ * out is [T, out_stride] in q's type, lse float[T][Hq] (may be NULL).  A query
+ * that sees no row gives out = 0 and lse = -infinity.  Rows of out and lse
+ * that belong to no sequence are not written.
+ *
+ * scores: NULL, or the cache's scores, to which each cached row's weight p,
+ * summed over the call's query tokens and the query heads that share the
+ * key/value head, is added.  (Sequences that share pages must then not be in
+ * one call: their additions would race.)
+ *
+ * Arithmetic: products of q (its own bits; fp32 in three bf16 parts) and whole
+ * codes are exact in fp32 sums; softmax statistics and sums are fp32.  The
+ * weights that multiply V are rounded to fp16 relative to the largest (bf16
+ * and FP8 outputs), or held in two fp16 parts (fp16 and fp32 outputs).
+ *
+ * workspace: device memory, 16-byte aligned, of at least the bytes that
+ * qknorm_kv4_attention_workspace gives for the same B, heads, D, dtype, max_q,
+ * max_pages * page_size and scores != NULL.
+ */
+int qknorm_kv4_attention(const void *q, int dtype, int64_t T, int Hq, int Hk, int D,
+                         int64_t row_stride, const void *pool, int64_t num_pages, int page_size,
+                         const int32_t *page_table, int64_t table_stride, int64_t max_pages,
+                         const int32_t *kv_lens, int64_t B, const int32_t *q_starts, int max_q,
+                         float scale, void *out, int64_t out_stride, float *lse, float *scores,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+
+int qknorm_kv4_attention_workspace(int64_t B, int dtype, int Hq, int Hk, int D, int max_q,
+                                   int64_t max_kv, int with_scores, int64_t *bytes);
+
+/*
+ * Eviction by accumulated attention weight.  For every sequence and key/value
+ * head, of n = kv_lens[b] rows, min(n, budget) are kept: the `recent` newest
+ * (0 <= recent <= budget) and, of the others, those with the highest scores
+ * (equal scores: the lower row first; a NaN score ranks below all).  The kept
+ * rows, codes, parameters and scores, are copied in their order to rows 0, 1,
+ * ... of the pages dst_table[b * dst_stride + 0 .. dst_pages) names, which
+ * must not be among the pages read; the old pages are the caller's to reuse.
+ * new_lens[b] becomes min(n, budget), and kept[b][h][0 .. budget) the kept
+ * rows' numbers, -1 behind the last.  dst_pages * page_size >= budget >= 1.
+ */
+int qknorm_kv4_evict(void *pool, int64_t num_pages, int page_size, int Hk, int D, float *scores,
+                     const int32_t *page_table, int64_t table_stride, int64_t max_pages,
+                     const int32_t *kv_lens, int64_t B, const int32_t *dst_table,
+                     int64_t dst_stride, int64_t dst_pages, int64_t budget, int64_t recent,
+                     int32_t *new_lens, int32_t *kept, void *stream);
+
+/* Pages and slots outside the pool that kernels met (and did not access) on
+ * the current device since the library was loaded; a blocking copy. */
+int qknorm_kv4_bad_pages(unsigned int *count);
+
+/* cudaError_t of the calling thread's last QKN_ERR_CUDA here (0 if none). */
+int qknorm_kv4_last_cuda_error(void);
+
+/* Version of this header's ABI: 100 * major + minor. */
+int qknorm_kv4_version(void);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* QKNORM_KV4_H */
