@@ -1,5 +1,26 @@
 // attention.cuh -- attention over the 4-bit cache.
 // Part of libqknorm.so; included by kv4.cu.
+//
+// The work is one pass over the cached rows: a row's D + 8 bytes meet a few
+// query rows (the group of query heads that share the key/value head, times
+// the call's query tokens).  At HBM speed an SM gets about 23 bytes a clock,
+// so what bounds the kernel beside HBM is the unpacking of the codes; the
+// products must not cost instructions too.  They are done by the warp-level
+// matrix instruction m16n8k16 with the CACHE as its 16-row operand and the
+// query rows as its 8-column one, both times:
+//
+//     S^T[16 rows, 8 queries] = (K codes - 8) . q^T       (k runs over D)
+//     O^T[16 of D, 8 queries] += (V codes - 8)^T . W^T    (k runs over rows)
+//
+// so that 8 query rows fill a tile (a tcgen05 tile would want 64 or 128, of
+// which decoding has 1 to 8), the codes go from a 32-bit word of 8 nibbles
+// straight into operand registers, and nothing passes through shared memory
+// between the two products: S^T leaves the first with a cached row to a lane
+// group, the weights are transposed by movmatrix into the second's operand.
+// A code minus 8 is a whole number from -8 to 7, exact in bf16 and fp16, and
+// the row's scale and middle come in on the 16x8 results:
+//     logit = scale_k * (q . (c - 8)) + mid_k * sum(q)
+//     out   = sum_j (p_j scale_v,j) (c_j - 8) + sum_j p_j mid_v,j
 #pragma once
 
 #include "cache.cuh"
@@ -20,8 +41,15 @@ struct AttentionArgs {
     float scale;
     void *out;
     float *lse;
-    float *row_lse;  // [B][max_q][Hq], in the workspace
     float *scores;
+    // Launch shape and workspace.
+    int direct;        // one block per item, no item is split
+    int max_items;     // items of a sequence at most (direct)
+    int log_rows;      // query rows of a logit record
+    float *part;       // [2 * blocks][rows][D]: sums of items split over blocks
+    float2 *part_ml;   // [2 * blocks][rows]: their maximum and sum
+    float2 *row_ml;    // [B][max_q * Hq]: each query row's maximum and 1 / sum (scores)
+    float *logits;     // [units][32][log_rows] (scores)
 };
 
 // Sequence b's cached rows and query tokens, taken into the ranges the buffers have.
@@ -31,159 +59,895 @@ __device__ __forceinline__ int kv_len(const AttentionArgs &a, int b)
     const int n = a.kv_lens[b];
     return n < 0 ? 0 : (n > most ? (int)most : n);
 }
-__device__ __forceinline__ void q_range(const AttentionArgs &a, int b, int64_t &start, int &count)
+__device__ __forceinline__ void q_range(const AttentionArgs &a, int b, int &start, int &count)
 {
     if (a.q_starts == nullptr) {
         start = b;
         count = 1;
         return;
     }
-    const int64_t s = a.q_starts[b], e = a.q_starts[b + 1];
-    start = s < 0 ? 0 : (s > a.T ? a.T : s);
-    const int64_t end = e < start ? start : (e > a.T ? a.T : e);
-    count = end - start > a.max_q ? a.max_q : (int)(end - start);
+    const int T = (int)a.T;
+    const int s = a.q_starts[b], e = a.q_starts[b + 1];
+    start = s < 0 ? 0 : (s > T ? T : s);
+    const int end = e < start ? start : (e > T ? T : e);
+    count = end - start > a.max_q ? a.max_q : end - start;
 }
 
-template <typename TS>
-__device__ __forceinline__ float load_one(const TS *p);
-template <>
-__device__ __forceinline__ float load_one(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-template <>
-__device__ __forceinline__ float load_one(const __half *p) { return __half2float(*p); }
-template <>
-__device__ __forceinline__ float load_one(const float *p) { return *p; }
-template <>
-__device__ __forceinline__ float load_one(const __nv_fp8_e4m3 *p) { return (float)*p; }
-__device__ __forceinline__ void store_one(__nv_bfloat16 *p, float f) { *p = __float2bfloat16_rn(f); }
-__device__ __forceinline__ void store_one(__half *p, float f) { *p = __float2half_rn(f); }
-__device__ __forceinline__ void store_one(float *p, float f) { *p = f; }
-__device__ __forceinline__ void store_one(__nv_fp8_e4m3 *p, float f) { *p = __nv_fp8_e4m3(f); }
+// ------------------------------------------------------------ work split --
+// A unit is 32 cached rows of one item; an item is one key/value head of a
+// sequence with up to kR of its query rows.  Units are numbered sequence by
+// sequence, item by item, and the blocks take equal runs of them, whatever
+// the lengths are: lengths are device data, and a batch of mixed lengths
+// splits as evenly as one of equal ones.  An item with no cached row still
+// has one (empty) unit, which writes its outputs.
+constexpr int kUnitRows = 32;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
 
-constexpr int kSimpleWarps = 4;
-
-// A row of the cache: lane l's D/32 elements and the row's pair.
-template <int D>
-__device__ __forceinline__ bool load_row(const AttentionArgs &a, const int32_t *table, int hk,
-                                         int kv, int j, int lane, float (&x)[D / 32])
+struct Seq {
+    int n, start, count;  // cached rows, first query token, query tokens
+    int items, units;     // items, and units of each
+};
+template <int kR>
+__device__ __forceinline__ Seq load_seq(const AttentionArgs &a, int b)
 {
-    const int64_t page = table[j >> a.pool.log2_page];
-    if (!page_ok(a.pool, page)) {
-        if (lane == 0) atomicAdd(&g_kv4_bad_pages, 1u);
-        return false;
-    }
-    const int off = j & ((1 << a.pool.log2_page) - 1);
-    const uint8_t *blk = a.pool.base + page * a.pool.page_bytes + (int64_t)hk * a.pool.head_bytes +
-                         (off / kBlockRows) * kBlockBytes<D>;
-    const int row = off % kBlockRows;
-    float scale, mid;
-    unpack_params(*reinterpret_cast<const uint32_t *>(blk + 16 * D + kv * 64 + row * 4), scale, mid);
-    const uint8_t *c = blk + kv * 8 * D + row * (D / 2) + lane * (D / 64);
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        x[2 * i] = fmaf(scale, (float)((int)(c[i] & 15) - 8), mid);
-        x[2 * i + 1] = fmaf(scale, (float)((int)(c[i] >> 4) - 8), mid);
-    }
-    return true;
+    Seq s;
+    s.n = kv_len(a, b);
+    q_range(a, b, s.start, s.count);
+    const int64_t rows = (int64_t)s.count * a.group;
+    s.items = (int)((rows + kR - 1) / kR) * a.pool.Hk;
+    s.units = s.n > 0 ? (s.n + kUnitRows - 1) / kUnitRows : 1;
+    return s;
 }
 
-// One block per (sequence, query token, query head); each warp takes every
-// fourth row with a softmax of its own, and the four are joined at the end.
-template <typename TS, int D>
-__global__ void __launch_bounds__(kSimpleWarps * 32)
-qkn_kv4_attention_kernel(AttentionArgs a)
-{
-    constexpr int kE = D / 32;
-    pdl_wait_then_release();
-    const int b = blockIdx.x, i = blockIdx.y, h = blockIdx.z;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int64_t start;
-    int count;
-    q_range(a, b, start, count);
-    if (i >= count) return;
-    const int sees = kv_len(a, b) - count + i + 1;
-    const int64_t t = start + i;
-    const int hk = h / a.group;
-    float q[kE], acc[kE] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e)
-        q[e] = load_one(static_cast<const TS *>(a.q) + t * a.row_stride + (int64_t)h * D +
-                        lane * kE + e);
-    const int32_t *table = a.page_table + b * a.table_stride;
-    for (int j = warp; j < sees; j += kSimpleWarps) {
-        float x[kE];
-        if (!load_row<D>(a, table, hk, 0, j, lane, x)) continue;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) s = fmaf(q[e], x[e], s);
-        s = group_sum<32>(s) * a.scale;
-        const float top = fmaxf(m, s);
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float old = expf(m - ref), p = expf(s - ref);
-        load_row<D>(a, table, hk, 1, j, lane, x);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) acc[e] = fmaf(acc[e], old, p * x[e]);
-        l = fmaf(l, old, p);
-        m = top;
+// A place in the sequence of units.
+template <int kR>
+struct Walk {
+    int b, item, unit, items, units, n;
+    __device__ __forceinline__ void load(const AttentionArgs &a)
+    {
+        const Seq s = load_seq<kR>(a, b);
+        items = s.items;
+        units = s.units;
+        n = s.n;
     }
-    __shared__ float part[kSimpleWarps][D + 2];
-#pragma unroll
-    for (int e = 0; e < kE; ++e) part[warp][lane * kE + e] = acc[e];
-    if (lane == 0) {
-        part[warp][D] = m;
-        part[warp][D + 1] = l;
-    }
-    __syncthreads();
-    float top = -INFINITY;
-    for (int w = 0; w < kSimpleWarps; ++w) top = fmaxf(top, part[w][D]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float total = 0.f;
-    for (int w = 0; w < kSimpleWarps; ++w) total += part[w][D + 1] * expf(part[w][D] - ref);
-    for (int d = threadIdx.x; d < D; d += kSimpleWarps * 32) {
-        float o = 0.f;
-        for (int w = 0; w < kSimpleWarps; ++w) o += part[w][d] * expf(part[w][D] - ref);
-        store_one(static_cast<TS *>(a.out) + t * a.out_stride + (int64_t)h * D + d,
-                  total == 0.f ? 0.f : o / total);
-    }
-    if (threadIdx.x == 0) {
-        const float lse = ref + logf(total);
-        if (a.lse != nullptr) a.lse[t * a.Hq + h] = lse;
-        a.row_lse[((int64_t)b * a.max_q + i) * a.Hq + h] = lse;
-    }
-}
-
-// One warp per cached row: its weight under every query row that sees it.
-template <typename TS, int D>
-__global__ void __launch_bounds__(kSimpleWarps * 32)
-qkn_kv4_scores_kernel(AttentionArgs a)
-{
-    constexpr int kE = D / 32;
-    pdl_wait_then_release();
-    const int b = blockIdx.x, hk = blockIdx.y;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int64_t start;
-    int count;
-    q_range(a, b, start, count);
-    const int n = kv_len(a, b);
-    const int32_t *table = a.page_table + b * a.table_stride;
-    for (int j = blockIdx.z * kSimpleWarps + warp; j < n; j += gridDim.z * kSimpleWarps) {
-        float x[kE], add = 0.f;
-        if (!load_row<D>(a, table, hk, 0, j, lane, x)) continue;
-        for (int i = 0; i < count; ++i) {
-            if (j >= n - count + i + 1) continue;
-            for (int g = 0; g < a.group; ++g) {
-                const int h = hk * a.group + g;
-                const TS *q = static_cast<const TS *>(a.q) + (start + i) * a.row_stride +
-                              (int64_t)h * D + lane * kE;
-                float s = 0.f;
-#pragma unroll
-                for (int e = 0; e < kE; ++e) s = fmaf(load_one(q + e), x[e], s);
-                s = group_sum<32>(s) * a.scale;
-                add += expf(s - a.row_lse[((int64_t)b * a.max_q + i) * a.Hq + h]);
+    // `count` units on; the caller stays within the batch's units.
+    __device__ __forceinline__ void step(const AttentionArgs &a, int count)
+    {
+        unit += count;
+        while (unit >= units) {
+            unit -= units;
+            if (++item >= items) {
+                item = 0;
+                do {
+                    if (++b >= a.B) return;
+                    load(a);
+                } while (items == 0);
             }
         }
-        const int64_t page = table[j >> a.pool.log2_page];
-        const int off = j & ((1 << a.pool.log2_page) - 1);
-        if (lane == 0) a.scores[((page * a.pool.Hk + hk) << a.pool.log2_page) + off] += add;
+    }
+};
+
+// The block's run of units [first, first + count) and where it begins; also
+// all sequences' units before sequence w.b.  Every block adds the lengths up
+// for itself (B numbers from L2).
+template <int kR>
+__device__ __forceinline__ int64_t block_run(const AttentionArgs &a, int64_t *scan, Walk<kR> &w,
+                                             int64_t &first, int &count)
+{
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = tid * per, b1 = min(a.B, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Seq s = load_seq<kR>(a, b);
+        mine += (int64_t)s.items * s.units;
+    }
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+    }
+    if (lane == 31) scan[warp] = sum;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += scan[i];
+        total += scan[i];
+    }
+    before += sum - mine;
+    // At most as many blocks as units take part, so that each has one.
+    const int64_t blocks = total < gridDim.x ? total : gridDim.x;
+    if (blockIdx.x < blocks) {
+        first = total * blockIdx.x / blocks;
+        count = (int)(total * (blockIdx.x + 1) / blocks - first);
+    } else {
+        first = count = 0;
+    }
+    if (count > 0 && first >= before && first < before + mine) {
+        int b = b0;
+        for (;; ++b) {  // ends: `first` lies in one of this thread's sequences
+            const Seq s = load_seq<kR>(a, b);
+            const int64_t u = (int64_t)s.items * s.units;
+            if (first < before + u) break;
+            before += u;
+        }
+        scan[kWarps] = b;
+        scan[kWarps + 1] = before;
+    }
+    __syncthreads();
+    w.b = 0;
+    if (count <= 0) return total;
+    w.b = (int)scan[kWarps];
+    w.load(a);
+    const int64_t in = first - scan[kWarps + 1];
+    w.item = (int)(in / w.units);
+    w.unit = (int)(in - (int64_t)w.item * w.units);
+    return total;
+}
+
+// ------------------------------------------------------------ instructions --
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <bool kBf16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    if constexpr (kBf16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
+{
+    return __byte_perm(a, b, sel);
+}
+
+// The four pairs (nibble p, nibble p + 4), p = 0..3, of a word as pairs of
+// whole numbers nibble - 8.  A nibble in the low mantissa bits of a power of
+// two is that power plus the nibble, so one subtraction (or, for fp16's
+// nibbles 16 times too high, one fma) leaves the number, exactly.
+template <bool kBf16>
+__device__ __forceinline__ void unpack_nibbles(uint32_t w, uint32_t (&o)[4])
+{
+    if constexpr (kBf16) {
+        const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));  // 136
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const uint32_t u = ((w >> (4 * p)) & 0x000f000fu) | 0x43004300u;  // 128 + c
+            const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u), off);
+            o[p] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+    } else {
+        const __half2 off = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));    // 1032
+        const __half2 sixteenth = __halves2half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00));
+        const __half2 off16 = __halves2half2(__ushort_as_half(0xd480), __ushort_as_half(0xd480));  // -72
+#pragma unroll
+        for (int p = 0; p < 4; p += 2) {
+            const uint32_t x = p == 0 ? w : w >> 8;
+            const uint32_t lo = (x & 0x000f000fu) | 0x64006400u;  // 1024 + c
+            const uint32_t hi = (x & 0x00f000f0u) | 0x64006400u;  // 1024 + 16 c
+            const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), off);
+            const __half2 b = __hfma2(*reinterpret_cast<const __half2 *>(&hi), sixteenth, off16);
+            o[p] = *reinterpret_cast<const uint32_t *>(&a);
+            o[p + 1] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+    }
+}
+
+// -------------------------------------------------------------- query rows --
+// The query operand holds q's own bits: bf16 as bf16, fp16 as fp16, FP8
+// widened to fp16, fp32 in three bf16 parts (8 + 8 + 8 significant bits).
+template <typename TS>
+struct QueryForm {
+    static constexpr bool kBf16 = true;
+    static constexpr int kParts = 1;
+};
+template <>
+struct QueryForm<float> {
+    static constexpr bool kBf16 = true;
+    static constexpr int kParts = 3;
+};
+template <>
+struct QueryForm<__half> {
+    static constexpr bool kBf16 = false;
+    static constexpr int kParts = 1;
+};
+template <>
+struct QueryForm<__nv_fp8_e4m3> {
+    static constexpr bool kBf16 = false;
+    static constexpr int kParts = 1;
+};
+// The weights that multiply V: fp16 (2^-11 relative), finer than the rounding
+// of a bf16 or FP8 output; in two fp16 parts where the output is finer.
+template <typename TS>
+constexpr int kWeightParts = 2;
+template <>
+constexpr int kWeightParts<__nv_bfloat16> = 1;
+template <>
+constexpr int kWeightParts<__nv_fp8_e4m3> = 1;
+
+// Eight consecutive elements as floats, and as the operand's pairs
+// (e_p, e_{p+4}), one set for each part.
+template <typename TS>
+__device__ __forceinline__ void load8(const TS *p, float (&f)[8])
+{
+    if constexpr (sizeof(TS) == 4) {
+        float lo[4], hi[4];
+        Storage<float>::unpack(*reinterpret_cast<const uint4 *>(p), lo);
+        Storage<float>::unpack(*(reinterpret_cast<const uint4 *>(p) + 1), hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f[e] = lo[e];
+            f[4 + e] = hi[e];
+        }
+    } else if constexpr (sizeof(TS) == 2) {
+        Storage<TS>::unpack(*reinterpret_cast<const uint4 *>(p), f);
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        e4m3x4_to_f32(u.x, f[0], f[1], f[2], f[3]);
+        e4m3x4_to_f32(u.y, f[4], f[5], f[6], f[7]);
+    }
+}
+template <typename TS>
+__device__ __forceinline__ void store8(TS *p, const float (&f)[8])
+{
+    if constexpr (sizeof(TS) == 4) {
+        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        *(reinterpret_cast<float4 *>(p) + 1) = make_float4(f[4], f[5], f[6], f[7]);
+    } else if constexpr (sizeof(TS) == 2) {
+        *reinterpret_cast<uint4 *>(p) = Storage<TS>::pack(f);
+    } else {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(f32_to_e4m3x4(f[0], f[1], f[2], f[3]),
+                                                   f32_to_e4m3x4(f[4], f[5], f[6], f[7]));
+    }
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    if constexpr (kBf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+template <typename TS>
+__device__ __forceinline__ void query_pairs(const float (&f)[8],
+                                            uint32_t (&o)[QueryForm<TS>::kParts][4])
+{
+    using F = QueryForm<TS>;
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = f[e];
+#pragma unroll
+    for (int part = 0; part < F::kParts; ++part) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) o[part][p] = pack2<F::kBf16>(r[p], r[p + 4]);
+        if constexpr (F::kParts > 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[e] -= __bfloat162float(__float2bfloat16_rn(r[e]));
+        }
+    }
+}
+
+// ------------------------------------------------------------- the kernel --
+// Shared memory: each warp's ring of units, then the block's join buffers.
+template <int D>
+constexpr int kUnitBytes = 2 * kBlockBytes<D>;
+template <int D>
+constexpr int kStages = D == 64 ? 3 : 2;
+template <int D, int NT>
+constexpr int kAttentionSmem = kWarps * kStages<D> * kUnitBytes<D> + 8 * NT * (D + 4) * 4 +
+                               3 * kWarps * 8 * NT * 4;
+
+constexpr float kWeightUnit = 16384.f;       // fp16 weights are held as up to this
+constexpr float kLeastScale = 7.7037197e-34f;  // 2^-110
+
+// Rows of the 16-row tile in the order that lets a warp read V without more
+// than two lanes on a bank: tile row r is the block's row row_of(r).
+__device__ __forceinline__ int row_of(int r) { return (r >> 1) + 4 * (r & 1); }
+
+template <typename TS, int D, int NT, bool kScores>
+__global__ void __launch_bounds__(kThreads, (D == 256 || NT > 1 || sizeof(TS) == 4 ? 2 : 4))
+qkn_kv4_attention_kernel(const AttentionArgs a)
+{
+    using F = QueryForm<TS>;
+    constexpr int kR = 8 * NT;
+    constexpr int kKSteps = D / 16, kMTiles = D / 16;
+    constexpr int kKWords = D / 32;  // a lane's words of a K row
+    constexpr int kVWords = D / 64;  // a lane's words of a V row
+    constexpr int kS = kStages<D>;
+    constexpr int kBB = kBlockBytes<D>;
+    constexpr int kChunks = kBB / 16;
+    constexpr int kWP = kWeightParts<TS>;
+
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int64_t scan[kWarps + 2];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int g = lane / 4, t = lane % 4;
+    uint8_t *ring = smem + warp * kS * kUnitBytes<D>;
+    float *join = reinterpret_cast<float *>(smem + kWarps * kS * kUnitBytes<D>);
+    float *join_m = join + kR * (D + 4);
+    float *join_l = join_m + kWarps * kR;
+    float *join_z = join_l + kWarps * kR;
+    pdl_wait_then_release();
+
+    Walk<kR> w;
+    int64_t first = 0;
+    int total = 0;
+    if (a.direct) {
+        w.b = blockIdx.x / a.max_items;
+        w.item = blockIdx.x - w.b * a.max_items;
+        w.unit = 0;
+        w.load(a);
+        if (w.item >= w.items) return;
+        total = w.units;
+    } else {
+        block_run<kR>(a, scan, w, first, total);
+        if (total <= 0) return;
+    }
+
+    // Loads run kS of the warp's units ahead of their use.
+    Walk<kR> ahead = w;
+    int next = warp;
+    if (next < total) ahead.step(a, warp);
+    uint32_t bad = 0;  // two bits a stage: blocks whose page is not in the pool
+    auto issue = [&](int stage) {
+        if (next < total) {
+            bad &= ~(3u << (2 * stage));
+            const int hk = ahead.item % a.pool.Hk;
+            const int row = ahead.unit * kUnitRows;
+            const int32_t *table = a.page_table + ahead.b * a.table_stride;
+            uint32_t to = smem_u32(ring + stage * kUnitBytes<D>) + lane * 16;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = row + half * kBlockRows;
+                if (r < ahead.n) {
+                    const int64_t page = table[r >> a.pool.log2_page];
+                    if (page_ok(a.pool, page)) {
+                        const int off = r & ((1 << a.pool.log2_page) - 1);
+                        const uint8_t *from = a.pool.base + page * a.pool.page_bytes +
+                                              (int64_t)hk * a.pool.head_bytes +
+                                              off / kBlockRows * kBB + lane * 16;
+#pragma unroll
+                        for (int c = 0; c < kChunks; c += 32)
+                            if (c + 32 <= kChunks || lane < kChunks - c)
+                                cp_async_s(to + c * 16, from + c * 16);
+                    } else {
+                        bad |= 1u << (2 * stage + half);
+                        if (lane == 0) atomicAdd(&g_kv4_bad_pages, 1u);
+                    }
+                }
+                to += kBB;
+            }
+            next += kWarps;
+            if (next < total) ahead.step(a, kWarps);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kS; ++s) issue(s);
+    int stage = 0;
+
+    // Items of the run, one after the other; `at` counts the run's units.
+    int at = 0, seg_index = 0;
+    while (at < total) {
+        const Seq seq = load_seq<kR>(a, w.b);
+        const int hk = w.item % a.pool.Hk, tile = w.item / a.pool.Hk;
+        const int rows = min(kR, seq.count * a.group - tile * kR);  // live query rows
+        const int seg_units = min(w.units - w.unit, total - at);
+        const bool whole = w.unit == 0 && seg_units == w.units;
+
+        // The query operand, and what each of the lane's columns needs.
+        uint32_t qf[NT][F::kParts][kKSteps][2];
+        float qsum[NT][2];
+        int vis[NT][2];
+        int all_see = seq.n;
+        const float c2 = a.scale * 1.4426950408889634f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + g;
+            const bool live = r < rows;
+            const int qr = live ? tile * kR + r : 0;
+            const int i = qr / a.group;
+            const TS *src = static_cast<const TS *>(a.q) + (int64_t)(seq.start + i) * a.row_stride +
+                            (int64_t)(hk * a.group + qr - i * a.group) * D + t * (D / 4);
+            float s = 0.f;
+#pragma unroll
+            for (int ww = 0; ww < kKWords; ++ww) {
+                float f[8] = {};
+                if (live) load8(src + ww * 8, f);
+                uint32_t pairs[F::kParts][4];
+                query_pairs<TS>(f, pairs);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += f[e];
+#pragma unroll
+                for (int part = 0; part < F::kParts; ++part)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        qf[nt][part][ww * 2 + p / 2][p % 2] = pairs[part][p];
+            }
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            int v = live ? seq.n - seq.count + i + 1 : seq.n;
+            all_see = min(all_see, v);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                qsum[nt][e] = __shfl_sync(0xffffffffu, s, (2 * t + e) * 4);
+                vis[nt][e] = __shfl_sync(0xffffffffu, v, (2 * t + e) * 4);
+            }
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o *= 2)
+            all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, o));
+
+        float acc[kMTiles][NT][4] = {};
+        float m[NT][2], l[NT][2] = {}, z[NT][2] = {};
+        float vref = kLeastScale;  // acc is in units of vref / kWeightUnit
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
+
+        // This warp's units of the item.
+        const int skip = (warp - at) & (kWarps - 1);
+        for (int k = skip; k < seg_units; k += kWarps) {
+            cp_async_wait<kS - 1>();
+            __syncwarp();
+            const uint8_t *unit = ring + stage * kUnitBytes<D>;
+            const int base = (w.unit + k) * kUnitRows;
+
+            float s[2][NT][4];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint8_t *blk = unit + half * kBB;
+                uint32_t kw[2][kKWords];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint8_t *p = blk + (row_of(g) + 8 * r) * (D / 2) + t * (D / 8);
+                    if constexpr (kKWords == 2) {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+                        kw[r][0] = u.x;
+                        kw[r][1] = u.y;
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < kKWords / 4; ++v) {
+                            const uint4 u = *(reinterpret_cast<const uint4 *>(p) + v);
+                            kw[r][4 * v] = u.x;
+                            kw[r][4 * v + 1] = u.y;
+                            kw[r][4 * v + 2] = u.z;
+                            kw[r][4 * v + 3] = u.w;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[half][nt][e] = 0.f;
+#pragma unroll
+                for (int ww = 0; ww < kKWords; ++ww) {
+                    uint32_t lo[4], hi[4];
+                    unpack_nibbles<F::kBf16>(kw[0][ww], lo);
+                    unpack_nibbles<F::kBf16>(kw[1][ww], hi);
+#pragma unroll
+                    for (int st = 0; st < 2; ++st)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int part = 0; part < F::kParts; ++part)
+                                mma<F::kBf16>(s[half][nt], lo[2 * st], hi[2 * st], lo[2 * st + 1],
+                                              hi[2 * st + 1], qf[nt][part][ww * 2 + st][0],
+                                              qf[nt][part][ww * 2 + st][1]);
+                }
+            }
+
+            // Logits in base 2, and the unit's largest.
+            float vs[2][2], vm[2][2];
+            const uint32_t bad_here = (bad >> (2 * stage)) & 3u;
+            const bool masked = base + kUnitRows > all_see || bad_here != 0;
+            float top[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+            float vtop = 0.f;
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = row_of(g) + 8 * r;
+                    const uint8_t *par = unit + half * kBB + 16 * D + row * 4;
+                    float ks, km;
+                    unpack_params(*reinterpret_cast<const uint32_t *>(par), ks, km);
+                    unpack_params(*reinterpret_cast<const uint32_t *>(par + 64), vs[half][r],
+                                  vm[half][r]);
+                    ks *= c2;
+                    km *= c2;
+                    const int j = base + half * kBlockRows + row;
+                    const bool gone = masked && (j >= seq.n || (bad_here >> half & 1u));
+                    if (gone) vs[half][r] = vm[half][r] = 0.f;
+                    vtop = fmaxf(vtop, vs[half][r]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float &x = s[half][nt][2 * r + e];
+                            x = fmaf(ks, x, km * qsum[nt][e]);
+                            if (masked && (gone || j >= vis[nt][e])) x = -INFINITY;
+                            top[nt][e] = fmaxf(top[nt][e], x);
+                        }
+                    if constexpr (kScores) {
+                        float *to = a.logits + ((first + at + k) * kUnitRows +
+                                                half * kBlockRows + row) * a.log_rows;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            if (nt * 8 + 2 * t < a.log_rows)
+                                *reinterpret_cast<float2 *>(to + nt * 8 + 2 * t) =
+                                    make_float2(s[half][nt][2 * r], s[half][nt][2 * r + 1]);
+                    }
+                }
+            bool grow = false;
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) {
+                vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], o));
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) grow = grow || top[nt][e] > m[nt][e];
+            grow = grow || vtop > vref;
+            if (__any_sync(0xffffffffu, grow)) {
+                // Bring what was summed so far to the new maxima.
+                float unit_scale = 1.f;
+                if (vtop > vref) {
+                    // The power of two above vtop; vtop is at most about 2^125.
+                    const uint32_t up = (__float_as_uint(vtop) & 0x7f800000u) + 0x00800000u;
+                    const int e = 127 + (int)(__float_as_uint(vref) >> 23) - (int)(up >> 23);
+                    unit_scale = e > 0 ? __uint_as_float((uint32_t)e << 23) : 0.f;
+                    vref = __uint_as_float(up);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mm = fmaxf(m[nt][e], top[nt][e]);
+                        const float f = mm == -INFINITY ? 1.f : exp2_approx(m[nt][e] - mm);
+                        m[nt][e] = mm;
+                        l[nt][e] *= f;
+                        z[nt][e] *= f;
+                        const float fa = f * unit_scale;
+#pragma unroll
+                        for (int mt = 0; mt < kMTiles; ++mt) {
+                            acc[mt][nt][e] *= fa;
+                            acc[mt][nt][2 + e] *= fa;
+                        }
+                    }
+            }
+
+            // Weights, transposed into the second product's operand.
+            // kWeightUnit / vref, both powers of two.
+            const float wscale =
+                __uint_as_float((2 * 127 + 14 - (__float_as_uint(vref) >> 23)) << 23);
+            uint32_t wf[2][NT][kWP][2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float sc = vs[half][r] * wscale;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float x[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float mm = m[nt][e];
+                            const float p =
+                                exp2_approx(s[half][nt][2 * r + e] - (mm == -INFINITY ? 0.f : mm));
+                            l[nt][e] += p;
+                            // A row that a query does not see adds nothing, whatever its
+                            // parameters are (NaN too).
+                            const bool seen = !masked || s[half][nt][2 * r + e] != -INFINITY;
+                            z[nt][e] = seen ? fmaf(p, vm[half][r], z[nt][e]) : z[nt][e];
+                            x[e] = seen ? p * sc : 0.f;
+                        }
+#pragma unroll
+                        for (int part = 0; part < kWP; ++part) {
+                            const __half2 h = __floats2half2_rn(x[0], x[1]);
+                            wf[half][nt][part][r] =
+                                transpose8x8(*reinterpret_cast<const uint32_t *>(&h));
+                            if constexpr (kWP > 1) {
+                                const float2 back = __half22float2(h);
+                                x[0] -= back.x;
+                                x[1] -= back.y;
+                            }
+                        }
+                    }
+                }
+
+            // O^T += V^T W^T: operand rows g and g + 8 of m-tile 4 * v + p are
+            // elements p and p + 4 of the lane's word v.
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint8_t *blk = unit + half * kBB + 8 * D + g * (D / 16);
+                uint32_t vw[4][kVWords];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint8_t *p = blk + (t + 4 * r) * (D / 2);
+                    if constexpr (kVWords == 1) {
+                        vw[r][0] = *reinterpret_cast<const uint32_t *>(p);
+                    } else if constexpr (kVWords == 2) {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+                        vw[r][0] = u.x;
+                        vw[r][1] = u.y;
+                    } else {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+                        vw[r][0] = u.x;
+                        vw[r][1] = u.y;
+                        vw[r][2] = u.z;
+                        vw[r][3] = u.w;
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < kVWords; ++v) {
+                    uint32_t x0[4], x1[4], x2[4], x3[4];
+                    unpack_nibbles<false>(prmt(vw[0][v], vw[1][v], 0x5410), x0);
+                    unpack_nibbles<false>(prmt(vw[0][v], vw[1][v], 0x7632), x1);
+                    unpack_nibbles<false>(prmt(vw[2][v], vw[3][v], 0x5410), x2);
+                    unpack_nibbles<false>(prmt(vw[2][v], vw[3][v], 0x7632), x3);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int part = 0; part < kWP; ++part)
+                                mma<false>(acc[4 * v + p][nt], x0[p], x1[p], x2[p], x3[p],
+                                           wf[half][nt][part][0], wf[half][nt][part][1]);
+                }
+            }
+            __syncwarp();
+            issue(stage);
+            stage = stage + 1 == kS ? 0 : stage + 1;
+        }
+
+        // Join the four warps, in order.
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) {
+                    l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
+                    z[nt][e] += __shfl_xor_sync(0xffffffffu, z[nt][e], o);
+                }
+                if (g == 0) {
+                    const int i = warp * kR + nt * 8 + 2 * t + e;
+                    join_m[i] = m[nt][e];
+                    join_l[i] = l[nt][e];
+                    join_z[i] = z[nt][e];
+                }
+            }
+        __syncthreads();
+        float f[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int col = nt * 8 + 2 * t + e;
+                float mm = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, join_m[i * kR + col]);
+                f[nt][e] = mm == -INFINITY
+                               ? 0.f
+                               : exp2_approx(m[nt][e] - mm) * (vref * (1.f / kWeightUnit));
+            }
+        for (int i = 0; i < kWarps; ++i) {
+            if (warp == i) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float *to = join + (nt * 8 + 2 * t + e) * (D + 4) + g * (D / 8);
+#pragma unroll
+                        for (int v = 0; v < kVWords; ++v)
+#pragma unroll
+                            for (int hi = 0; hi < 2; ++hi) {
+                                float4 *p = reinterpret_cast<float4 *>(to + v * 8 + hi * 4);
+                                float4 x = i > 0 ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
+                                const int c = 2 * hi + e;
+                                x.x = fmaf(acc[4 * v][nt][c], f[nt][e], x.x);
+                                x.y = fmaf(acc[4 * v + 1][nt][c], f[nt][e], x.y);
+                                x.z = fmaf(acc[4 * v + 2][nt][c], f[nt][e], x.z);
+                                x.w = fmaf(acc[4 * v + 3][nt][c], f[nt][e], x.w);
+                                *p = x;
+                            }
+                    }
+            }
+            __syncthreads();
+        }
+        // Eight elements of a row to a thread.
+        const int slot = 2 * blockIdx.x + (seg_index > 0 ? 1 : 0);
+        for (int i = tid; i < rows * (D / 8); i += kThreads) {
+            const int r = i / (D / 8), d = (i % (D / 8)) * 8;
+            float mm = -INFINITY, ll = 0.f, zz = 0.f;
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) mm = fmaxf(mm, join_m[v * kR + r]);
+#pragma unroll
+            for (int v = 0; v < kWarps; ++v) {
+                const float e = mm == -INFINITY ? 0.f : exp2_approx(join_m[v * kR + r] - mm);
+                ll = fmaf(join_l[v * kR + r], e, ll);
+                zz = fmaf(join_z[v * kR + r], e, zz);
+            }
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = join[r * (D + 4) + d + e] + zz;
+            if (whole) {
+                const float inv = ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = ll == 0.f ? 0.f : o[e] * inv;
+                const int qr = tile * kR + r;
+                const int qi = qr / a.group, h = hk * a.group + qr - qi * a.group;
+                store8(static_cast<TS *>(a.out) + (int64_t)(seq.start + qi) * a.out_stride +
+                           (int64_t)h * D + d,
+                       o);
+                if (d == 0) {
+                    if (a.lse != nullptr)
+                        a.lse[(int64_t)(seq.start + qi) * a.Hq + h] =
+                            ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+                    if constexpr (kScores)
+                        a.row_ml[(int64_t)w.b * a.max_q * a.Hq + qi * a.Hq + h] =
+                            make_float2(ll == 0.f ? 0.f : mm, inv);
+                }
+            } else {
+                float *to = a.part + ((int64_t)slot * kR + r) * D + d;
+                store8(to, o);
+                if (d == 0) a.part_ml[(int64_t)slot * kR + r] = make_float2(mm, ll);
+            }
+        }
+        __syncthreads();
+        at += seg_units;
+        seg_index = 1;
+        if (at < total) w.step(a, seg_units);
+    }
+    cp_async_wait<0>();
+}
+
+// Joins the items whose units were split over blocks: one warp to a query
+// row, the parts added in the blocks' order.
+template <typename TS, int D, int kR, bool kScores>
+__global__ void __launch_bounds__(kThreads)
+qkn_kv4_join_kernel(const AttentionArgs a)
+{
+    constexpr int kE = D / 32;
+    __shared__ int64_t scan[kWarps + 2];
+    pdl_wait_then_release();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    // The parts of a block are those of its run's first and last items; each
+    // split item is joined by the block that holds its first unit, which
+    // finds it as the last item of its run.
+    Walk<kR> w;
+    int64_t first;
+    int total;
+    const int64_t all = block_run<kR>(a, scan, w, first, total);
+    if (total <= 0) return;
+    int slot = 2 * blockIdx.x;
+    int left = total;  // units from w on
+    while (left > w.units - w.unit) {
+        left -= w.units - w.unit;
+        // Skip whole items of the same sequence in one step.
+        w.unit = 0;
+        if (++w.item >= w.items) {
+            w.item = 0;
+            do {
+                ++w.b;
+                w.load(a);
+            } while (w.items == 0);
+        }
+        const int more = min(w.items - 1 - w.item, (left - 1) / w.units);
+        w.item += more;
+        left -= more * w.units;
+        slot = 2 * blockIdx.x + 1;
+    }
+    // The last item of the run: does it begin here, and go on in later blocks?
+    if (w.unit != 0 || left == w.units) return;
+    const int64_t last_unit = first + total - left + w.units - 1;
+    const int64_t blocks = all < gridDim.x ? all : gridDim.x;
+    const int last = (int)(((last_unit + 1) * blocks - 1) / all);
+    const Seq seq = load_seq<kR>(a, w.b);
+    const int hk = w.item % a.pool.Hk, tile = w.item / a.pool.Hk;
+    const int rows = min(kR, seq.count * a.group - tile * kR);
+    for (int r = warp; r < rows; r += kWarps) {
+        float mm = -INFINITY;
+        for (int c = blockIdx.x + lane; c <= last; c += 32)
+            mm = fmaxf(mm, a.part_ml[(int64_t)(c == blockIdx.x ? slot : 2 * c) * kR + r].x);
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        float o[kE] = {}, ll = 0.f;
+        for (int c = blockIdx.x; c <= last; ++c) {
+            const int64_t at = (int64_t)(c == (int)blockIdx.x ? slot : 2 * c) * kR + r;
+            const float2 ml = a.part_ml[at];
+            const float e = mm == -INFINITY ? 0.f : exp2_approx(ml.x - mm);
+            ll = fmaf(ml.y, e, ll);
+#pragma unroll
+            for (int i = 0; i < kE; ++i) o[i] = fmaf(a.part[at * D + lane * kE + i], e, o[i]);
+        }
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        const int qr = tile * kR + r;
+        const int qi = qr / a.group, h = hk * a.group + qr - qi * a.group;
+        TS *to = static_cast<TS *>(a.out) + (int64_t)(seq.start + qi) * a.out_stride +
+                 (int64_t)h * D + lane * kE;
+#pragma unroll
+        for (int i = 0; i < kE; ++i) to[i] = (TS)(ll == 0.f ? 0.f : o[i] * inv);
+        if (lane == 0) {
+            if (a.lse != nullptr)
+                a.lse[(int64_t)(seq.start + qi) * a.Hq + h] =
+                    ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+            if constexpr (kScores)
+                a.row_ml[(int64_t)w.b * a.max_q * a.Hq + qi * a.Hq + h] =
+                    make_float2(ll == 0.f ? 0.f : mm, inv);
+        }
+    }
+}
+
+// Adds each cached row's weight to its score: a warp to a unit, a lane to a
+// row, over all the items of the unit's key/value head.
+template <int kR>
+__global__ void __launch_bounds__(kThreads) qkn_kv4_scores_kernel(const AttentionArgs a)
+{
+    __shared__ int64_t scan[kWarps + 2];
+    pdl_wait_then_release();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    Walk<kR> w;
+    int64_t first;
+    int total;
+    block_run<kR>(a, scan, w, first, total);
+    for (int k = 0; k < total; ++k) {
+        // The units of a head's first tile stand for the head.
+        if (w.item < a.pool.Hk && (k % kWarps) == warp) {
+            const Seq seq = load_seq<kR>(a, w.b);
+            const int hk = w.item;
+            const int j = w.unit * kUnitRows + lane;
+            if (j < seq.n) {
+                const int64_t page =
+                    a.page_table[w.b * a.table_stride + (j >> a.pool.log2_page)];
+                if (page_ok(a.pool, page)) {
+                    float add = 0.f;
+                    const int64_t tile_units = (int64_t)a.pool.Hk * w.units;
+                    const float *x = a.logits + ((first + k) * kUnitRows + lane) * a.log_rows;
+                    const float2 *ml = a.row_ml + (int64_t)w.b * a.max_q * a.Hq;
+                    const int rows = seq.count * a.group;
+                    for (int r = 0; r < rows; ++r) {
+                        const int qi = r / a.group, h = hk * a.group + r - qi * a.group;
+                        const float2 f = ml[qi * a.Hq + h];
+                        const float v =
+                            x[(int64_t)(r / kR) * tile_units * kUnitRows * a.log_rows + r % kR];
+                        add = fmaf(exp2_approx(v - f.x), f.y, add);
+                    }
+                    const int off = j & ((1 << a.pool.log2_page) - 1);
+                    a.scores[((page * a.pool.Hk + hk) << a.pool.log2_page) + off] += add;
+                }
+            }
+        }
+        if (k + 1 < total) w.step(a, 1);
     }
 }
 

@@ -172,16 +172,116 @@ struct Read {
     }
 };
 
+// -------------------------------------------------------------- attention --
+constexpr int kMaxBlocks = 1024;  // of the attention kernel (four to an SM at most)
+// Items of at most this many units are not split: one launch instead of two.
+constexpr int64_t kDirectUnits = 16;
+
+// Query tiles (of 8 columns) of an item: as many as the rows of a key/value
+// head fill, as the register budget allows (the query operand and the sums of
+// a tile take D/16 * (2 * parts + 4) registers).
+int query_tiles(int dtype, int D, int64_t rows)
+{
+    const int parts = dtype == QKN_FP32 ? 3 : 1;
+    int nt = 1;
+    while (nt < 4 && rows > 8 * nt && 2 * nt * (D / 16) * (2 * parts + 4) <= 192) nt *= 2;
+    return nt;
+}
+
+struct AttentionPlan {
+    int nt, log_rows, max_items;
+    bool direct;
+    int64_t max_units;  // of an item
+    int64_t part, part_ml, row_ml, logits, bytes;  // offsets in the workspace, and its size
+};
+
+AttentionPlan attention_plan(int64_t B, int dtype, int Hq, int Hk, int D, int max_q,
+                             int64_t max_kv, bool scores)
+{
+    AttentionPlan p = {};
+    const int64_t rows = (int64_t)max_q * (Hq / Hk);
+    p.nt = query_tiles(dtype, D, rows);
+    const int64_t kr = 8 * p.nt;
+    const int64_t tiles = (rows + kr - 1) / kr;
+    p.max_units = max_kv > 0 ? (max_kv + kUnitRows - 1) / kUnitRows : 1;
+    p.max_items = (int)(tiles * Hk);
+    p.direct = !scores && p.max_units <= kDirectUnits && B * tiles * Hk <= INT32_MAX;
+    p.log_rows = (int)(rows < kr ? (rows + 1) / 2 * 2 : kr);
+    // Sizes may pass 63 bits for arguments that no buffer could have.
+    __int128 at = 0;
+    p.part = 0;
+    at += (__int128)2 * kMaxBlocks * kr * D * 4;
+    p.part_ml = (int64_t)at;
+    at += (__int128)2 * kMaxBlocks * kr * 8;
+    p.row_ml = (int64_t)at;
+    if (scores) {
+        at += ((__int128)B * max_q * Hq * 8 + 15) / 16 * 16;
+        p.logits = at > INT64_MAX ? INT64_MAX : (int64_t)at;
+        at += (__int128)B * tiles * Hk * p.max_units * kUnitRows * p.log_rows * 4;
+    }
+    p.bytes = at > INT64_MAX ? INT64_MAX : (int64_t)at;
+    return p;
+}
+
+// Resident blocks of a kernel on an SM, looked up once for each device with
+// its shared-memory limit raised.
+template <typename Kern>
+int blocks_per_sm(Kern kern, int smem, std::atomic<int> *cache, int *out)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 0 || dev >= kMaxDevices) return QKN_ERR_UNSUPPORTED;
+    int n = cache[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (n < 1) return QKN_ERR_UNSUPPORTED;
+        cache[dev].store(n, std::memory_order_release);
+    }
+    *out = n;
+    return QKN_OK;
+}
+
+template <typename TS, int D, int NT, bool kScores>
+int launch_attention(const AttentionArgs &a, const AttentionPlan &p, cudaStream_t stream)
+{
+    static std::atomic<int> cache[kMaxDevices];
+    constexpr int smem = kAttentionSmem<D, NT>;
+    auto kern = qkn_kv4_attention_kernel<TS, D, NT, kScores>;
+    int per_sm = 0, sms = 0, rc;
+    if ((rc = device_sms(&sms)) != QKN_OK) return rc;
+    if ((rc = blocks_per_sm(kern, smem, cache, &per_sm)) != QKN_OK) return rc;
+    if (p.direct)
+        return launch(kern, dim3((unsigned)(a.B * (int64_t)p.max_items)), kThreads, smem, stream, a);
+    const int64_t units = (int64_t)a.B * p.max_items * p.max_units;
+    int64_t grid = (int64_t)sms * per_sm;
+    if (grid > kMaxBlocks) grid = kMaxBlocks;
+    if (grid > units) grid = units;
+    const dim3 blocks((unsigned)grid);
+    if ((rc = launch(kern, blocks, kThreads, smem, stream, a)) != QKN_OK) return rc;
+    rc = launch(qkn_kv4_join_kernel<TS, D, 8 * NT, kScores>, blocks, kThreads, 0, stream, a);
+    if (rc != QKN_OK || !kScores) return rc;
+    return launch(qkn_kv4_scores_kernel<8 * NT>, blocks, kThreads, 0, stream, a);
+}
+
 struct Attention {
     template <typename TS, int D>
-    static int run(AttentionArgs a, cudaStream_t stream)
+    static int run(AttentionArgs a, AttentionPlan p, cudaStream_t stream)
     {
-        int rc = launch(qkn_kv4_attention_kernel<TS, D>,
-                        dim3((unsigned)a.B, (unsigned)a.max_q, (unsigned)a.Hq), kSimpleWarps * 32, 0,
-                        stream, a);
-        if (rc != QKN_OK || a.scores == nullptr) return rc;
-        return launch(qkn_kv4_scores_kernel<TS, D>, dim3((unsigned)a.B, (unsigned)a.pool.Hk, 64u),
-                      kSimpleWarps * 32, 0, stream, a);
+        constexpr int kTile = D / 16 * (2 * QueryForm<TS>::kParts + 4);
+#define QKN_KV4_NT(NT)                                                                         \
+    if constexpr (NT == 1 || NT * kTile <= 192)                                                \
+        if (p.nt == NT)                                                                        \
+            return a.scores != nullptr ? launch_attention<TS, D, NT, true>(a, p, stream)       \
+                                       : launch_attention<TS, D, NT, false>(a, p, stream);
+        QKN_KV4_NT(1)
+        QKN_KV4_NT(2)
+        QKN_KV4_NT(4)
+#undef QKN_KV4_NT
+        return QKN_ERR_UNSUPPORTED;
     }
 };
 
@@ -193,12 +293,6 @@ int attention_shape(int64_t B, int dtype, int Hq, int Hk, int D, int max_q, int6
         max_q > 65535 || max_kv < 0 || max_kv > INT32_MAX)
         return QKN_ERR_SHAPE;
     return QKN_OK;
-}
-
-int64_t attention_workspace(int64_t B, int dtype, int Hq, int Hk, int D, int max_q,
-                            int64_t max_kv, int with_scores)
-{
-    return (int64_t)4 * B * max_q * Hq + 16;
 }
 
 }  // namespace
@@ -250,7 +344,7 @@ int qknorm_kv4_attention_workspace(int64_t B, int dtype, int Hq, int Hk, int D, 
     *bytes = 0;
     const int rc = attention_shape(B, dtype, Hq, Hk, D, max_q, max_kv);
     if (rc != QKN_OK) return rc;
-    *bytes = attention_workspace(B, dtype, Hq, Hk, D, max_q, max_kv, with_scores);
+    *bytes = attention_plan(B, dtype, Hq, Hk, D, max_q, max_kv, with_scores != 0).bytes;
     return QKN_OK;
 }
 
@@ -280,9 +374,9 @@ int qknorm_kv4_attention(const void *q, int dtype, int64_t T, int Hq, int Hk, in
         !aligned(page_table, 4) || !aligned(kv_lens, 4) || !aligned(q_starts, 4) ||
         !aligned(lse, 4) || !aligned(scores, 4))
         return QKN_ERR_ALIGN;
-    if (workspace_bytes <
-        attention_workspace(B, dtype, Hq, Hk, D, max_q, max_pages * page_size, scores != nullptr))
-        return QKN_ERR_SHAPE;
+    const AttentionPlan plan =
+        attention_plan(B, dtype, Hq, Hk, D, max_q, max_pages * page_size, scores != nullptr);
+    if (workspace_bytes < plan.bytes) return QKN_ERR_SHAPE;
     AttentionArgs a = {};
     a.q = q;
     a.T = T;
@@ -301,9 +395,16 @@ int qknorm_kv4_attention(const void *q, int dtype, int64_t T, int Hq, int Hk, in
     a.scale = scale;
     a.out = out;
     a.lse = lse;
-    a.row_lse = static_cast<float *>(workspace);
     a.scores = scores;
-    return by_type<Attention>(dtype, D, a, static_cast<cudaStream_t>(stream));
+    a.direct = plan.direct;
+    a.max_items = plan.max_items;
+    a.log_rows = plan.log_rows;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.part = reinterpret_cast<float *>(ws + plan.part);
+    a.part_ml = reinterpret_cast<float2 *>(ws + plan.part_ml);
+    a.row_ml = reinterpret_cast<float2 *>(ws + plan.row_ml);
+    a.logits = reinterpret_cast<float *>(ws + plan.logits);
+    return by_type<Attention>(dtype, D, a, plan, static_cast<cudaStream_t>(stream));
 }
 
 int qknorm_kv4_evict(void *pool, int64_t num_pages, int page_size, int Hk, int D, float *scores,
