@@ -17,11 +17,13 @@
 // straight into operand registers, and nothing passes through shared memory
 // between the two products: S^T leaves the first with a cached row to a lane
 // group, the weights are transposed by movmatrix into the second's operand.
-// A code minus 8 is a whole number from -8 to 7, exact in bf16 and fp16, and
-// the row's scale and middle come in on the 16x8 results:
+// The codes are whole numbers, exact in fp16, and the row's scale and middle
+// come in on the 16x8 results:
 //     logit = scale_k * (q . (c - 8)) + mid_k * sum(q)
 //     out   = sum_j (p_j scale_v,j) (c_j - 8) + sum_j p_j mid_v,j
 #pragma once
+
+#include <type_traits>
 
 #include "cache.cuh"
 
@@ -201,41 +203,36 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-template <bool kBf16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    if constexpr (kBf16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
 {
     return __byte_perm(a, b, sel);
 }
 
-// The four pairs (nibble p, nibble p + 4), p = 0..3, of a word as pairs of
-// whole numbers nibble - 8.  A nibble in the low mantissa bits of a power of
-// two is that power plus the nibble, so one subtraction (or, for fp16's
-// nibbles 16 times too high, one fma) leaves the number, exactly.
-template <bool kBf16>
+// The four pairs (nibble p, nibble p + 4), p = 0..3, of a word of codes as
+// fp16 operands, in one of two forms.
+// Raw: the nibbles where they lie, read as subnormal numbers: c * 2^-24 for
+// even p and c * 2^-20 for odd p.  One logic instruction a pair; the power of
+// two and the 8 are made up for elsewhere.
+// Centred: c - 8.  A nibble in the low mantissa bits of a power of two is that
+// power plus the nibble, so one subtraction (or one fma for the nibbles that
+// lie 4 bits higher) leaves the number, exactly.
+template <bool kRaw>
 __device__ __forceinline__ void unpack_nibbles(uint32_t w, uint32_t (&o)[4])
 {
-    if constexpr (kBf16) {
-        const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));  // 136
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const uint32_t u = ((w >> (4 * p)) & 0x000f000fu) | 0x43004300u;  // 128 + c
-            const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u), off);
-            o[p] = *reinterpret_cast<const uint32_t *>(&v);
-        }
+    if constexpr (kRaw) {
+        const uint32_t x = w >> 8;
+        o[0] = w & 0x000f000fu;
+        o[1] = w & 0x00f000f0u;
+        o[2] = x & 0x000f000fu;
+        o[3] = x & 0x00f000f0u;
     } else {
         const __half2 off = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));    // 1032
         const __half2 sixteenth = __halves2half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00));
@@ -254,28 +251,19 @@ __device__ __forceinline__ void unpack_nibbles(uint32_t w, uint32_t (&o)[4])
 }
 
 // -------------------------------------------------------------- query rows --
-// The query operand holds q's own bits: bf16 as bf16, fp16 as fp16, FP8
-// widened to fp16, fp32 in three bf16 parts (8 + 8 + 8 significant bits).
+// The query operand is fp16, after one power of two for all the rows of an
+// item that brings the largest element to [2^14, 2^15).  bf16 (8 significant
+// bits), fp16 and FP8 elements keep all their bits down to 2^-31 of the
+// largest; what is smaller is off by less than 2^-39 of it, far below the
+// rounding of an fp32 sum.  fp32 elements are held in two parts of 11 bits.
 template <typename TS>
-struct QueryForm {
-    static constexpr bool kBf16 = true;
-    static constexpr int kParts = 1;
-};
-template <>
-struct QueryForm<float> {
-    static constexpr bool kBf16 = true;
-    static constexpr int kParts = 3;
-};
-template <>
-struct QueryForm<__half> {
-    static constexpr bool kBf16 = false;
-    static constexpr int kParts = 1;
-};
-template <>
-struct QueryForm<__nv_fp8_e4m3> {
-    static constexpr bool kBf16 = false;
-    static constexpr int kParts = 1;
-};
+constexpr int kQueryParts = sizeof(TS) == 4 ? 2 : 1;
+constexpr int kQueryExp = 14;
+// Keys as raw codes: q . c is summed from 0 for every unit, and 8 * sum(q) is
+// taken off in fp32.  fp32 queries use centred codes, whose sums are smaller
+// and so lose less.
+template <typename TS>
+constexpr bool kRawKeys = sizeof(TS) != 4;
 // The weights that multiply V: fp16 (2^-11 relative), finer than the rounding
 // of a bf16 or FP8 output; in two fp16 parts where the output is finer.
 template <typename TS>
@@ -284,6 +272,12 @@ template <>
 constexpr int kWeightParts<__nv_bfloat16> = 1;
 template <>
 constexpr int kWeightParts<__nv_fp8_e4m3> = 1;
+// Values as raw codes: each 16 rows' sums get -8 times their weights from a
+// product with a constant operand, which costs a matrix instruction where the
+// subtraction from four operand registers would cost four others.  That pays
+// while there is one query tile and one part.
+template <typename TS, int NT>
+constexpr bool kRawValues = NT == 1 && kWeightParts<TS> == 1;
 
 // Eight consecutive elements as floats, and as the operand's pairs
 // (e_p, e_{p+4}), one set for each part.
@@ -320,35 +314,28 @@ __device__ __forceinline__ void store8(TS *p, const float (&f)[8])
                                                    f32_to_e4m3x4(f[4], f[5], f[6], f[7]));
     }
 }
-template <bool kBf16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
-{
-    if constexpr (kBf16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    } else {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
-}
+// Elements (p, p + 4) as an operand register, part by part; odd pairs meet
+// raw codes that are 16 times too large.
 template <typename TS>
-__device__ __forceinline__ void query_pairs(const float (&f)[8],
-                                            uint32_t (&o)[QueryForm<TS>::kParts][4])
+__device__ __forceinline__ void query_pairs(const float (&f)[8], float factor,
+                                            uint32_t (&o)[kQueryParts<TS>][4])
 {
-    using F = QueryForm<TS>;
-    float r[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = f[e];
+    for (int p = 0; p < 4; ++p) {
+        const float by = kRawKeys<TS> && p % 2 ? factor * 0.0625f : factor;
+        float x = f[p] * by, y = f[p + 4] * by;
 #pragma unroll
-    for (int part = 0; part < F::kParts; ++part) {
-#pragma unroll
-        for (int p = 0; p < 4; ++p) o[part][p] = pack2<F::kBf16>(r[p], r[p + 4]);
-        if constexpr (F::kParts > 1) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] -= __bfloat162float(__float2bfloat16_rn(r[e]));
+        for (int part = 0; part < kQueryParts<TS>; ++part) {
+            const __half2 h = __floats2half2_rn(x, y);
+            o[part][p] = *reinterpret_cast<const uint32_t *>(&h);
+            const float2 back = __half22float2(h);
+            x -= back.x;
+            y -= back.y;
         }
     }
 }
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
 
 // ------------------------------------------------------------- the kernel --
 // Shared memory: each warp's ring of units, then the block's join buffers.
@@ -360,26 +347,32 @@ template <int D, int NT>
 constexpr int kAttentionSmem = kWarps * kStages<D> * kUnitBytes<D> + 8 * NT * (D + 4) * 4 +
                                3 * kWarps * 8 * NT * 4;
 
-constexpr float kWeightUnit = 16384.f;       // fp16 weights are held as up to this
+// A weight is held as p * 2^kWeightExp * (scale_v / vref), p relative to a
+// maximum that may lag behind by 2^kLag, so that it is rarely moved: at most
+// 2^14, and exact to 2^-11 down to 2^-20 of the largest.
+constexpr int kWeightExp = 6;
+constexpr float kLag = 8.f;
 constexpr float kLeastScale = 7.7037197e-34f;  // 2^-110
 
-// Rows of the 16-row tile in the order that lets a warp read V without more
-// than two lanes on a bank: tile row r is the block's row row_of(r).
+// Rows of the 16-row tile in an order that lets a warp read V with at most two
+// lanes on a bank: tile row r is the block's row row_of(r).
 __device__ __forceinline__ int row_of(int r) { return (r >> 1) + 4 * (r & 1); }
 
 template <typename TS, int D, int NT, bool kScores>
 __global__ void __launch_bounds__(kThreads, (D == 256 || NT > 1 || sizeof(TS) == 4 ? 2 : 4))
 qkn_kv4_attention_kernel(const AttentionArgs a)
 {
-    using F = QueryForm<TS>;
     constexpr int kR = 8 * NT;
+    constexpr int kQP = kQueryParts<TS>;
+    constexpr int kWP = kWeightParts<TS>;
+    constexpr bool kRawK = kRawKeys<TS>;
+    constexpr bool kRawV = kRawValues<TS, NT>;
     constexpr int kKSteps = D / 16, kMTiles = D / 16;
     constexpr int kKWords = D / 32;  // a lane's words of a K row
     constexpr int kVWords = D / 64;  // a lane's words of a V row
     constexpr int kS = kStages<D>;
     constexpr int kBB = kBlockBytes<D>;
     constexpr int kChunks = kBB / 16;
-    constexpr int kWP = kWeightParts<TS>;
 
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int64_t scan[kWarps + 2];
@@ -407,41 +400,59 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
         if (total <= 0) return;
     }
 
-    // Loads run kS of the warp's units ahead of their use.
+    // Loads run kS of the warp's units ahead of their use, and the page
+    // numbers of a unit are read one unit before it is loaded.
     Walk<kR> ahead = w;
     int next = warp;
-    if (next < total) ahead.step(a, warp);
+    const int32_t *table = nullptr;
+    const uint8_t *head = nullptr;
+    int page[2] = {-1, -1};
+    auto look = [&] {  // where `ahead` is
+        const int row = ahead.unit * kUnitRows;
+        page[0] = row < ahead.n ? table[row >> a.pool.log2_page] : -2;
+        page[1] = row + kBlockRows < ahead.n ? table[(row + kBlockRows) >> a.pool.log2_page] : -2;
+    };
+    auto enter = [&] {  // a new item
+        table = a.page_table + ahead.b * a.table_stride;
+        head = a.pool.base + (int64_t)(ahead.item % a.pool.Hk) * a.pool.head_bytes + lane * 16;
+    };
+    if (next < total) {
+        ahead.step(a, warp);
+        enter();
+        look();
+    }
     uint32_t bad = 0;  // two bits a stage: blocks whose page is not in the pool
+    const uint32_t page_mask = (1u << a.pool.log2_page) - 1;
     auto issue = [&](int stage) {
         if (next < total) {
             bad &= ~(3u << (2 * stage));
-            const int hk = ahead.item % a.pool.Hk;
-            const int row = ahead.unit * kUnitRows;
-            const int32_t *table = a.page_table + ahead.b * a.table_stride;
-            uint32_t to = smem_u32(ring + stage * kUnitBytes<D>) + lane * 16;
+            const uint32_t to = smem_u32(ring + stage * kUnitBytes<D>) + lane * 16;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int r = row + half * kBlockRows;
-                if (r < ahead.n) {
-                    const int64_t page = table[r >> a.pool.log2_page];
-                    if (page_ok(a.pool, page)) {
-                        const int off = r & ((1 << a.pool.log2_page) - 1);
-                        const uint8_t *from = a.pool.base + page * a.pool.page_bytes +
-                                              (int64_t)hk * a.pool.head_bytes +
-                                              off / kBlockRows * kBB + lane * 16;
+                if ((uint32_t)page[half] < (uint32_t)a.pool.pages) {
+                    const uint32_t off =
+                        (uint32_t)(ahead.unit * kUnitRows + half * kBlockRows) & page_mask;
+                    const uint8_t *from = head +
+                                          (uint64_t)(uint32_t)page[half] * (uint32_t)a.pool.page_bytes +
+                                          off / kBlockRows * kBB;
 #pragma unroll
-                        for (int c = 0; c < kChunks; c += 32)
-                            if (c + 32 <= kChunks || lane < kChunks - c)
-                                cp_async_s(to + c * 16, from + c * 16);
-                    } else {
-                        bad |= 1u << (2 * stage + half);
-                        if (lane == 0) atomicAdd(&g_kv4_bad_pages, 1u);
-                    }
+                    for (int c = 0; c < kChunks; c += 32)
+                        if (c + 32 <= kChunks || lane < kChunks - c)
+                            cp_async_s(to + half * kBB + c * 16, from + c * 16);
+                } else if (ahead.unit * kUnitRows + half * kBlockRows < ahead.n) {
+                    bad |= 1u << (2 * stage + half);
+                    if (lane == 0) atomicAdd(&g_kv4_bad_pages, 1u);
                 }
-                to += kBB;
             }
             next += kWarps;
-            if (next < total) ahead.step(a, kWarps);
+            if (next < total) {
+                ahead.unit += kWarps;
+                if (ahead.unit >= ahead.units) {
+                    ahead.step(a, 0);
+                    enter();
+                }
+                look();
+            }
         }
         cp_async_commit();
     };
@@ -458,60 +469,80 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
         const int seg_units = min(w.units - w.unit, total - at);
         const bool whole = w.unit == 0 && seg_units == w.units;
 
-        // The query operand, and what each of the lane's columns needs.
-        uint32_t qf[NT][F::kParts][kKSteps][2];
+        // The query operand, and what each of the lane's columns needs.  Two
+        // passes over the rows: the largest element, then the operand.
+        uint32_t qf[NT][kQP][kKSteps][2];
         float qsum[NT][2];
         int vis[NT][2];
         int all_see = seq.n;
         const float c2 = a.scale * 1.4426950408889634f;
+        float largest = 0.f, factor = 1.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = nt * 8 + g;
-            const bool live = r < rows;
-            const int qr = live ? tile * kR + r : 0;
-            const int i = qr / a.group;
-            const TS *src = static_cast<const TS *>(a.q) + (int64_t)(seq.start + i) * a.row_stride +
-                            (int64_t)(hk * a.group + qr - i * a.group) * D + t * (D / 4);
-            float s = 0.f;
+        for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
-            for (int ww = 0; ww < kKWords; ++ww) {
-                float f[8] = {};
-                if (live) load8(src + ww * 8, f);
-                uint32_t pairs[F::kParts][4];
-                query_pairs<TS>(f, pairs);
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = nt * 8 + g;
+                const bool live = r < rows;
+                const int qr = live ? tile * kR + r : 0;
+                const int i = qr / a.group;
+                const TS *src = static_cast<const TS *>(a.q) +
+                                (int64_t)(seq.start + i) * a.row_stride +
+                                (int64_t)(hk * a.group + qr - i * a.group) * D + t * (D / 4);
+                float s = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += f[e];
+                for (int ww = 0; ww < kKWords; ++ww) {
+                    float f[8] = {};
+                    if (live) load8(src + ww * 8, f);
+                    if (pass == 0) {
 #pragma unroll
-                for (int part = 0; part < F::kParts; ++part)
+                        for (int e = 0; e < 8; ++e)
+                            if (fabsf(f[e]) <= 3.402823466e38f) largest = fmaxf(largest, fabsf(f[e]));
+                    } else {
+                        uint32_t pairs[kQP][4];
+                        query_pairs<TS>(f, factor, pairs);
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        qf[nt][part][ww * 2 + p / 2][p % 2] = pairs[part][p];
+                        for (int e = 0; e < 8; ++e) s += f[e];
+#pragma unroll
+                        for (int part = 0; part < kQP; ++part)
+#pragma unroll
+                            for (int p = 0; p < 4; ++p)
+                                qf[nt][part][ww * 2 + p / 2][p % 2] = pairs[part][p];
+                    }
+                }
+                if (pass == 0) continue;
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                s *= c2;
+                const int v = live ? seq.n - seq.count + i + 1 : seq.n;
+                all_see = min(all_see, v);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    qsum[nt][e] = __shfl_sync(0xffffffffu, s, (2 * t + e) * 4);
+                    vis[nt][e] = __shfl_sync(0xffffffffu, v, (2 * t + e) * 4);
+                }
             }
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            int v = live ? seq.n - seq.count + i + 1 : seq.n;
-            all_see = min(all_see, v);
+            if (pass == 0) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                qsum[nt][e] = __shfl_sync(0xffffffffu, s, (2 * t + e) * 4);
-                vis[nt][e] = __shfl_sync(0xffffffffu, v, (2 * t + e) * 4);
+                for (int o = 1; o < 32; o *= 2)
+                    largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+                factor = power_of_two(min(max(kQueryExp - exponent_of(largest), -103), 113));
             }
         }
 #pragma unroll
         for (int o = 4; o < 32; o *= 2)
             all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, o));
+        // What the product of the operands has to be multiplied by.
+        const float c_s = c2 * power_of_two((kRawK ? 24 : 0) - exponent_of(factor));
 
         float acc[kMTiles][NT][4] = {};
         float m[NT][2], l[NT][2] = {}, z[NT][2] = {};
-        float vref = kLeastScale;  // acc is in units of vref / kWeightUnit
+        float vref = kLeastScale;  // a power of two, at least the largest scale of V so far
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
 
-        // This warp's units of the item.
-        const int skip = (warp - at) & (kWarps - 1);
-        for (int k = skip; k < seg_units; k += kWarps) {
-            cp_async_wait<kS - 1>();
-            __syncwarp();
+        // One unit; kMask: some of its rows are hidden from some of the queries.
+        auto consume = [&](auto mask_tag, const int k) {
+            constexpr bool kMask = decltype(mask_tag)::value;
             const uint8_t *unit = ring + stage * kUnitBytes<D>;
             const int base = (w.unit + k) * kUnitRows;
 
@@ -545,24 +576,23 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
 #pragma unroll
                 for (int ww = 0; ww < kKWords; ++ww) {
                     uint32_t lo[4], hi[4];
-                    unpack_nibbles<F::kBf16>(kw[0][ww], lo);
-                    unpack_nibbles<F::kBf16>(kw[1][ww], hi);
+                    unpack_nibbles<kRawK>(kw[0][ww], lo);
+                    unpack_nibbles<kRawK>(kw[1][ww], hi);
 #pragma unroll
                     for (int st = 0; st < 2; ++st)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int part = 0; part < F::kParts; ++part)
-                                mma<F::kBf16>(s[half][nt], lo[2 * st], hi[2 * st], lo[2 * st + 1],
-                                              hi[2 * st + 1], qf[nt][part][ww * 2 + st][0],
-                                              qf[nt][part][ww * 2 + st][1]);
+                            for (int part = 0; part < kQP; ++part)
+                                mma(s[half][nt], lo[2 * st], hi[2 * st], lo[2 * st + 1],
+                                    hi[2 * st + 1], qf[nt][part][ww * 2 + st][0],
+                                    qf[nt][part][ww * 2 + st][1]);
                 }
             }
 
-            // Logits in base 2, and the unit's largest.
+            // Logits in base 2, and the lane's largest.
             float vs[2][2], vm[2][2];
-            const uint32_t bad_here = (bad >> (2 * stage)) & 3u;
-            const bool masked = base + kUnitRows > all_see || bad_here != 0;
+            const uint32_t bad_here = kMask ? (bad >> (2 * stage)) & 3u : 0u;
             float top[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
@@ -577,10 +607,10 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                     unpack_params(*reinterpret_cast<const uint32_t *>(par), ks, km);
                     unpack_params(*reinterpret_cast<const uint32_t *>(par + 64), vs[half][r],
                                   vm[half][r]);
-                    ks *= c2;
-                    km *= c2;
+                    if constexpr (kRawK) km = fmaf(-8.f, ks, km);
+                    ks *= c_s;
                     const int j = base + half * kBlockRows + row;
-                    const bool gone = masked && (j >= seq.n || (bad_here >> half & 1u));
+                    const bool gone = kMask && (j >= seq.n || (bad_here >> half & 1u));
                     if (gone) vs[half][r] = vm[half][r] = 0.f;
                     vtop = fmaxf(vtop, vs[half][r]);
 #pragma unroll
@@ -589,7 +619,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                         for (int e = 0; e < 2; ++e) {
                             float &x = s[half][nt][2 * r + e];
                             x = fmaf(ks, x, km * qsum[nt][e]);
-                            if (masked && (gone || j >= vis[nt][e])) x = -INFINITY;
+                            if (kMask && (gone || j >= vis[nt][e])) x = -INFINITY;
                             top[nt][e] = fmaxf(top[nt][e], x);
                         }
                     if constexpr (kScores) {
@@ -602,30 +632,29 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                                     make_float2(s[half][nt][2 * r], s[half][nt][2 * r + 1]);
                     }
                 }
-            bool grow = false;
-#pragma unroll
-            for (int o = 4; o < 32; o *= 2) {
-                vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], o));
-            }
+            bool grow = vtop > vref;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) grow = grow || top[nt][e] > m[nt][e];
-            grow = grow || vtop > vref;
+                for (int e = 0; e < 2; ++e) grow = grow || top[nt][e] > m[nt][e] + kLag;
             if (__any_sync(0xffffffffu, grow)) {
                 // Bring what was summed so far to the new maxima.
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) {
+                    vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            top[nt][e] =
+                                fmaxf(top[nt][e], __shfl_xor_sync(0xffffffffu, top[nt][e], o));
+                }
                 float unit_scale = 1.f;
                 if (vtop > vref) {
-                    // The power of two above vtop; vtop is at most about 2^125.
-                    const uint32_t up = (__float_as_uint(vtop) & 0x7f800000u) + 0x00800000u;
-                    const int e = 127 + (int)(__float_as_uint(vref) >> 23) - (int)(up >> 23);
-                    unit_scale = e > 0 ? __uint_as_float((uint32_t)e << 23) : 0.f;
-                    vref = __uint_as_float(up);
+                    // The power of two above vtop (which is at most about 2^125).
+                    const int e = exponent_of(vtop) + 1, down = exponent_of(vref) - e;
+                    unit_scale = down >= -126 ? power_of_two(down) : 0.f;
+                    vref = power_of_two(e);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -646,29 +675,33 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
             }
 
             // Weights, transposed into the second product's operand.
-            // kWeightUnit / vref, both powers of two.
-            const float wscale =
-                __uint_as_float((2 * 127 + 14 - (__float_as_uint(vref) >> 23)) << 23);
+            const float wscale = power_of_two(kWeightExp - exponent_of(vref));
             uint32_t wf[2][NT][kWP][2];
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int nt = 0; nt < NT; ++nt) {
+                const float m0 = kMask && m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+                const float m1 = kMask && m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float sc = vs[half][r] * wscale;
+                for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
+                    for (int r = 0; r < 2; ++r) {
+                        const float sc = vs[half][r] * wscale;
                         float x[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float mm = m[nt][e];
-                            const float p =
-                                exp2_approx(s[half][nt][2 * r + e] - (mm == -INFINITY ? 0.f : mm));
+                            const float logit = s[half][nt][2 * r + e];
+                            const float p = exp2_approx(logit - (e ? m1 : m0));
                             l[nt][e] += p;
-                            // A row that a query does not see adds nothing, whatever its
-                            // parameters are (NaN too).
-                            const bool seen = !masked || s[half][nt][2 * r + e] != -INFINITY;
-                            z[nt][e] = seen ? fmaf(p, vm[half][r], z[nt][e]) : z[nt][e];
-                            x[e] = seen ? p * sc : 0.f;
+                            if constexpr (kMask) {
+                                // A row that a query does not see adds nothing, whatever
+                                // its parameters are (NaN too).
+                                const bool seen = logit != -INFINITY;
+                                z[nt][e] = seen ? fmaf(p, vm[half][r], z[nt][e]) : z[nt][e];
+                                x[e] = seen ? p * sc : 0.f;
+                            } else {
+                                z[nt][e] = fmaf(p, vm[half][r], z[nt][e]);
+                                x[e] = p * sc;
+                            }
                         }
 #pragma unroll
                         for (int part = 0; part < kWP; ++part) {
@@ -682,7 +715,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                             }
                         }
                     }
-                }
+            }
 
             // O^T += V^T W^T: operand rows g and g + 8 of m-tile 4 * v + p are
             // elements p and p + 4 of the lane's word v.
@@ -710,20 +743,37 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
 #pragma unroll
                 for (int v = 0; v < kVWords; ++v) {
                     uint32_t x0[4], x1[4], x2[4], x3[4];
-                    unpack_nibbles<false>(prmt(vw[0][v], vw[1][v], 0x5410), x0);
-                    unpack_nibbles<false>(prmt(vw[0][v], vw[1][v], 0x7632), x1);
-                    unpack_nibbles<false>(prmt(vw[2][v], vw[3][v], 0x5410), x2);
-                    unpack_nibbles<false>(prmt(vw[2][v], vw[3][v], 0x7632), x3);
+                    unpack_nibbles<kRawV>(prmt(vw[0][v], vw[1][v], 0x5410), x0);
+                    unpack_nibbles<kRawV>(prmt(vw[0][v], vw[1][v], 0x7632), x1);
+                    unpack_nibbles<kRawV>(prmt(vw[2][v], vw[3][v], 0x5410), x2);
+                    unpack_nibbles<kRawV>(prmt(vw[2][v], vw[3][v], 0x7632), x3);
 #pragma unroll
                     for (int p = 0; p < 4; ++p)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int part = 0; part < kWP; ++part)
-                                mma<false>(acc[4 * v + p][nt], x0[p], x1[p], x2[p], x3[p],
-                                           wf[half][nt][part][0], wf[half][nt][part][1]);
+                            for (int part = 0; part < kWP; ++part) {
+                                const uint32_t b0 = wf[half][nt][part][0], b1 = wf[half][nt][part][1];
+                                mma(acc[4 * v + p][nt], x0[p], x1[p], x2[p], x3[p], b0, b1);
+                                if constexpr (kRawV) {
+                                    // -8, as large as the tile's raw codes are.
+                                    const uint32_t c = p % 2 ? 0x80808080u : 0x80088008u;
+                                    mma(acc[4 * v + p][nt], c, c, c, c, b0, b1);
+                                }
+                            }
                 }
             }
+        };
+
+        // This warp's units of the item.
+        const int skip = (warp - at) & (kWarps - 1);
+        for (int k = skip; k < seg_units; k += kWarps) {
+            cp_async_wait<kS - 1>();
+            __syncwarp();
+            if ((w.unit + k + 1) * kUnitRows > all_see || (bad >> (2 * stage) & 3u))
+                consume(std::true_type{}, k);
+            else
+                consume(std::false_type{}, k);
             __syncwarp();
             issue(stage);
             stage = stage + 1 == kS ? 0 : stage + 1;
@@ -756,17 +806,19 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                 float mm = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, join_m[i * kR + col]);
-                f[nt][e] = mm == -INFINITY
-                               ? 0.f
-                               : exp2_approx(m[nt][e] - mm) * (vref * (1.f / kWeightUnit));
+                f[nt][e] = mm == -INFINITY ? 0.f : exp2_approx(m[nt][e] - mm) * vref;
             }
         for (int i = 0; i < kWarps; ++i) {
             if (warp == i) {
+                // The sums' own power of two (odd tiles of raw codes: 16 times less).
+                constexpr float kEven = (kRawV ? 16777216.f : 1.f) / (1 << kWeightExp);
+                constexpr float kOdd = kRawV ? kEven / 16.f : kEven;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float *to = join + (nt * 8 + 2 * t + e) * (D + 4) + g * (D / 8);
+                        const float by = f[nt][e];
 #pragma unroll
                         for (int v = 0; v < kVWords; ++v)
 #pragma unroll
@@ -774,10 +826,10 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                                 float4 *p = reinterpret_cast<float4 *>(to + v * 8 + hi * 4);
                                 float4 x = i > 0 ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
                                 const int c = 2 * hi + e;
-                                x.x = fmaf(acc[4 * v][nt][c], f[nt][e], x.x);
-                                x.y = fmaf(acc[4 * v + 1][nt][c], f[nt][e], x.y);
-                                x.z = fmaf(acc[4 * v + 2][nt][c], f[nt][e], x.z);
-                                x.w = fmaf(acc[4 * v + 3][nt][c], f[nt][e], x.w);
+                                x.x = fmaf(acc[4 * v][nt][c] * kEven, by, x.x);
+                                x.y = fmaf(acc[4 * v + 1][nt][c] * kOdd, by, x.y);
+                                x.z = fmaf(acc[4 * v + 2][nt][c] * kEven, by, x.z);
+                                x.w = fmaf(acc[4 * v + 3][nt][c] * kOdd, by, x.w);
                                 *p = x;
                             }
                     }

@@ -86,7 +86,8 @@ int check_pool(const void *pool, int64_t num_pages, int page_size, int Hk, int D
     while (log2_page < 8 && (1 << log2_page) != page_size) ++log2_page;
     if ((1 << log2_page) != page_size) return QKN_ERR_SHAPE;
     const int64_t head = (int64_t)(page_size / kBlockRows) * (16 * D + 128);
-    if (num_pages > INT64_MAX / head / Hk) return QKN_ERR_SHAPE;
+    // The kernels number pages and the bytes of one in 32 bits.
+    if (num_pages > INT32_MAX || head * Hk > INT32_MAX) return QKN_ERR_SHAPE;
     if (pool == nullptr) return QKN_ERR_NULL;
     if (!aligned(pool, 16)) return QKN_ERR_ALIGN;
     out->base = static_cast<uint8_t *>(const_cast<void *>(pool));
@@ -182,7 +183,7 @@ constexpr int64_t kDirectUnits = 16;
 // a tile take D/16 * (2 * parts + 4) registers).
 int query_tiles(int dtype, int D, int64_t rows)
 {
-    const int parts = dtype == QKN_FP32 ? 3 : 1;
+    const int parts = dtype == QKN_FP32 ? 2 : 1;
     int nt = 1;
     while (nt < 4 && rows > 8 * nt && 2 * nt * (D / 16) * (2 * parts + 4) <= 192) nt *= 2;
     return nt;
@@ -271,7 +272,7 @@ struct Attention {
     template <typename TS, int D>
     static int run(AttentionArgs a, AttentionPlan p, cudaStream_t stream)
     {
-        constexpr int kTile = D / 16 * (2 * QueryForm<TS>::kParts + 4);
+        constexpr int kTile = D / 16 * (2 * kQueryParts<TS> + 4);
 #define QKN_KV4_NT(NT)                                                                         \
     if constexpr (NT == 1 || NT * kTile <= 192)                                                \
         if (p.nt == NT)                                                                        \

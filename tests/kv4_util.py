@@ -112,7 +112,12 @@ def attend(cache, q, Hq, table, lens, starts, scale, dtype):
             mids = np.einsum("hgn,hn->hg", p, np.abs(mv[:, s]))[..., None]
             floor = (2.0 ** -25 if part == 2.0 ** -11 else 2.0 ** -35) * 8
             least = floor * sees * sv[:, s].max(-1)[:, None, None] / total
-            bound[t] = part * mag + least + (rel + (sees + 16) * 2.0 ** -23) * (mag + mids)
+            # A sum may be taken over the codes c themselves with 8 times the
+            # weights taken off: its terms are then up to |c - 8| + 8 in size,
+            # and each addition rounds (or truncates) at 2^-23 of that.
+            eights = 8 * np.einsum("hgn,hn->hg", p, sv[:, s])[..., None]
+            bound[t] = (part * mag + least + rel * (mag + mids)
+                        + (sees + 16) * 2.0 ** -23 * (mag + eights + mids))
             j = np.arange(sees)
             at = np.asarray(pages)[j // page]
             add[at, :, j % page] += p.sum(1).T
