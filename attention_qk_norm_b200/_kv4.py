@@ -11,7 +11,7 @@ import ctypes
 import threading
 
 from . import _binding
-from ._binding import QKNormError, _dtype_code, _gamma_ptr
+from ._binding import QKNormError
 
 _lock = threading.Lock()
 _kv4_lib = None
@@ -55,35 +55,40 @@ def _check(fn, rc):
                           lib.qknorm_kv4_last_cuda_error())
 
 
-class _On:
-    """Makes a device and, where one is given, a stream current for a call."""
+# torch and what the wrappers use of it, looked up on the first call: decoding
+# calls them once a layer and token, so their own time counts.
+torch = None
+_codes = _raw_stream = _device_now = None
+
+
+def _torch():
+    global torch, _codes, _raw_stream, _device_now
+    if torch is None:
+        import torch as module
+
+        _codes = {module.bfloat16: _binding.QKN_BF16, module.float32: _binding.QKN_FP32,
+                  module.float16: _binding.QKN_FP16, module.float8_e4m3fn: _binding.QKN_FP8_E4M3}
+        _raw_stream = getattr(module._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: module.cuda.current_stream(index).cuda_stream)
+        _device_now = module.cuda.current_device
+        torch = module
+    return torch
+
+
+class _Elsewhere:
+    """Makes a device and, where one is given, a stream current."""
 
     def __init__(self, device, stream):
-        import torch
-
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError("stream belongs to %s, the tensors live on %s"
-                                 % (stream.device, device))
-            self._ctx = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self._ctx = torch.cuda.device(device)
-        else:
-            self._ctx = None
+        if stream is not None and stream.device != device:
+            raise ValueError("stream belongs to %s, the tensors live on %s"
+                             % (stream.device, device))
+        self._ctx = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
+        self._ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-
-
-def _stream_of(device):
-    import torch
-
-    return torch.cuda.current_stream(device).cuda_stream
+        self._ctx.__exit__(*exc)
 
 
 class KV4Cache:
@@ -92,34 +97,38 @@ class KV4Cache:
     for eviction, ``scores`` (float32 [num_pages, Hk, page_size]).  The tensors
     are the caller's; ``KV4Cache.empty`` allocates them, scores zeroed."""
 
-    __slots__ = ("pool", "scores", "Hk", "D", "page_size", "num_pages")
+    __slots__ = ("pool", "scores", "Hk", "D", "page_size", "num_pages", "index", "_pool_ptr",
+                 "_scores_ptr")
 
     def __init__(self, pool, Hk, D, page_size=64, scores=None):
-        import torch
-
+        _torch()
         if D not in HEAD_DIMS:
             raise ValueError("D must be 64, 128 or 256, got %r" % (D,))
         if page_size not in PAGE_SIZES:
             raise ValueError("page_size must be one of %s, got %r" % (PAGE_SIZES, page_size))
-        if not pool.is_cuda:
+        index = pool.get_device()
+        if index < 0:
             raise ValueError("pool must be a CUDA tensor (QK-Norm runs only on the GPU)")
-        shape = (pool.shape[0], Hk, page_size // 16, 16 * D + 128)
-        if pool.dtype != torch.uint8 or tuple(pool.shape) != shape or not pool.is_contiguous():
+        shape = pool.shape
+        pages = shape[0]
+        if (pool.dtype is not torch.uint8 or shape != (pages, Hk, page_size // 16, 16 * D + 128)
+                or not pool.is_contiguous()):
             raise ValueError("pool must be a contiguous uint8 tensor [num_pages, Hk, "
                              "page_size // 16, 16 * D + 128]")
-        if scores is not None:
-            if (scores.dtype != torch.float32 or not scores.is_contiguous()
-                    or tuple(scores.shape) != (shape[0], Hk, page_size)
-                    or scores.device != pool.device):
-                raise ValueError("scores must be a contiguous float32 tensor [num_pages, Hk, "
-                                 "page_size] on the pool's device")
+        if scores is not None and (
+                scores.dtype is not torch.float32 or not scores.is_contiguous()
+                or scores.shape != (pages, Hk, page_size) or scores.get_device() != index):
+            raise ValueError("scores must be a contiguous float32 tensor [num_pages, Hk, "
+                             "page_size] on the pool's device")
         self.pool, self.scores = pool, scores
-        self.Hk, self.D, self.page_size, self.num_pages = Hk, D, page_size, shape[0]
+        self.Hk, self.D, self.page_size, self.num_pages = Hk, D, page_size, pages
+        self.index = index
+        self._pool_ptr = pool.data_ptr()
+        self._scores_ptr = None if scores is None else scores.data_ptr()
 
     @classmethod
     def empty(cls, num_pages, Hk, D, page_size=64, scores=False, device="cuda"):
-        import torch
-
+        _torch()
         if D not in HEAD_DIMS or page_size not in PAGE_SIZES:
             raise ValueError("D must be one of %s and page_size one of %s"
                              % (HEAD_DIMS, PAGE_SIZES))
@@ -131,39 +140,52 @@ class KV4Cache:
         return cls(pool, Hk, D, page_size, sums)
 
 
-def _vec(t, name, dtype, n, device):
+def _vec(t, name, dtype, n, index):
     """A device vector of ``n`` elements with unit stride."""
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError("%s must be a contiguous %s vector of %d elements" % (name, dtype, n))
-    if t.device != device:
-        raise ValueError("%s must live on the cache's device" % name)
+    if (t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()
+            or t.get_device() != index):
+        raise ValueError("%s must be a contiguous %s vector of %d elements on the cache's device"
+                         % (name, dtype, n))
     return t.data_ptr()
 
 
-def _table(t, name, B, device):
-    import torch
-
-    if t.dtype != torch.int32 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("%s must be an int32 tensor [B, pages] with unit column stride" % name)
-    if t.shape[0] != B or t.device != device:
-        raise ValueError("%s must have one row for each sequence, on the cache's device" % name)
-    # One row (or one column) may come with any stride in torch.
-    stride = t.stride(0) if B > 1 else t.shape[1]
-    return t.data_ptr(), stride, t.shape[1]
-
-
-def _fused(t, name, device):
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor (QK-Norm runs only on the GPU)" % name)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("%s must be a 2-D [T, row_stride] view with unit column stride" % name)
-    if t.device != device:
-        raise ValueError("%s must live on the cache's device" % name)
-    return t.shape[0], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(t, name, index):
+    """A 2-D view with unit column stride on the cache's device: its sizes and
+    row stride (one row may come with any stride in torch)."""
+    if t.get_device() != index:
+        raise ValueError("%s must be a CUDA tensor on the cache's device" % name)
+    if t.dim() != 2:
+        raise ValueError("%s must be two-dimensional" % name)
+    n, width = t.shape
+    stride, unit = t.stride()
+    if unit != 1 and width > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    return n, width, stride if n > 1 else width
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _table(t, name, B, index):
+    n, pages, stride = _rows(t, name, index)
+    if t.dtype is not torch.int32 or n != B:
+        raise ValueError("%s must be an int32 tensor [B, pages]" % name)
+    return t.data_ptr(), stride, pages
+
+
+def _code(t, name):
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be bfloat16, float32, float16 or float8_e4m3fn, got %s"
+                        % (name, t.dtype))
+    return code
+
+
+def _weights(g, name, D, index):
+    if g is None:
+        return None
+    if g.dtype is not torch.float32 or not g.is_contiguous():
+        raise TypeError("%s must be a contiguous float32 tensor" % name)
+    if g.numel() != D or g.get_device() != index:
+        raise ValueError("%s must have D elements on the cache's device" % name)
+    return g.data_ptr()
 
 
 def kv4_bad_pages() -> int:
@@ -178,21 +200,19 @@ def qknorm_kv4_append(cache, qkv, slots, Hq, gamma_q=None, gamma_k=None, eps=1e-
     """Per-head QK-Norm in place on ``qkv`` [T, row_stride] with its key and
     value rows stored in the cache, token t at slot ``slots[t]`` (int64; a
     negative slot stores nothing).  Without weights nothing is normalised."""
-    import torch
-
-    dev = cache.pool.device
-    T, stride = _fused(qkv, "qkv", dev)
-    sp = _vec(slots, "slots", torch.int64, T, dev)
-    for g in (gamma_q, gamma_k):
-        if g is not None and (g.device != dev or g.numel() != cache.D):
-            raise ValueError("gamma_q and gamma_k must have D elements on the cache's device")
-    with _On(dev, stream):
-        rc = _lib().qknorm_kv4_append(
-            qkv.data_ptr(), _dtype_code(qkv), T, Hq, cache.Hk, cache.D, stride,
-            _gamma_ptr(gamma_q, "gamma_q"), _gamma_ptr(gamma_k, "gamma_k"), eps, sp,
-            cache.pool.data_ptr(), cache.num_pages, cache.page_size, _ptr(cache.scores),
-            _stream_of(dev))
-    _check("qknorm_kv4_append", rc)
+    index = cache.index
+    if stream is not None or _device_now() != index:
+        with _Elsewhere(cache.pool.device, stream):
+            return qknorm_kv4_append(cache, qkv, slots, Hq, gamma_q, gamma_k, eps)
+    T, _, stride = _rows(qkv, "qkv", index)
+    D = cache.D
+    rc = (_kv4_lib or _lib()).qknorm_kv4_append(
+        qkv.data_ptr(), _code(qkv, "qkv"), T, Hq, cache.Hk, D, stride,
+        _weights(gamma_q, "gamma_q", D, index), _weights(gamma_k, "gamma_k", D, index), eps,
+        _vec(slots, "slots", torch.int64, T, index), cache._pool_ptr, cache.num_pages,
+        cache.page_size, cache._scores_ptr, _raw_stream(index))
+    if rc:
+        _check("qknorm_kv4_append", rc)
     return qkv
 
 
@@ -200,38 +220,34 @@ def qknorm_kv4_read(cache, slots, dtype=None, stream=None):
     """The rows that ``slots`` (int64 [N]) hold, as values of ``dtype``
     (default bfloat16): ``(k, v)``, each [N, Hk * D].  A slot outside the pool
     reads as zeros."""
-    import torch
-
-    dev = cache.pool.device
-    if slots.dim() != 1:
-        raise ValueError("slots must be a vector")
-    N, width = slots.shape[0], cache.Hk * cache.D
-    sp = _vec(slots, "slots", torch.int64, N, dev)
-    with _On(dev, stream):
-        k = torch.empty((N, width), dtype=dtype or torch.bfloat16, device=dev)
-        v = torch.empty_like(k)
-        rc = _lib().qknorm_kv4_read(
-            cache.pool.data_ptr(), cache.num_pages, cache.page_size, cache.Hk, cache.D, sp, N,
-            k.data_ptr(), v.data_ptr(), _dtype_code(k), width, _stream_of(dev))
-    _check("qknorm_kv4_read", rc)
+    index = cache.index
+    if stream is not None or _device_now() != index:
+        with _Elsewhere(cache.pool.device, stream):
+            return qknorm_kv4_read(cache, slots, dtype)
+    N, width = slots.numel(), cache.Hk * cache.D
+    sp = _vec(slots, "slots", torch.int64, N, index)
+    k, v = cache.pool.new_empty((2, N, width), dtype=dtype or torch.bfloat16).unbind(0)
+    rc = (_kv4_lib or _lib()).qknorm_kv4_read(
+        cache._pool_ptr, cache.num_pages, cache.page_size, cache.Hk, cache.D, sp, N, k.data_ptr(),
+        v.data_ptr(), _code(k, "dtype"), width, _raw_stream(index))
+    if rc:
+        _check("qknorm_kv4_read", rc)
     return k, v
 
 
-def _workspace_bytes(B, dtype, Hq, cache, max_q, max_kv, with_scores):
+def _workspace_bytes(B, code, Hq, cache, max_q, max_kv, with_scores):
     n = ctypes.c_int64(0)
     _check("qknorm_kv4_attention_workspace", _lib().qknorm_kv4_attention_workspace(
-        B, dtype, Hq, cache.Hk, cache.D, max_q, max_kv, int(with_scores), ctypes.byref(n)))
+        B, code, Hq, cache.Hk, cache.D, max_q, max_kv, int(with_scores), ctypes.byref(n)))
     return n.value
 
 
 def kv4_attention_workspace(cache, qkv, Hq, page_table, max_q=1, add_scores=False):
     """A workspace for ``qknorm_kv4_attention`` with these arguments, to keep
     for calls that do not overlap on the GPU."""
-    import torch
-
-    n = _workspace_bytes(page_table.shape[0], _dtype_code(qkv), Hq, cache, max_q,
+    n = _workspace_bytes(page_table.shape[0], _code(qkv, "qkv"), Hq, cache, max_q,
                          page_table.shape[1] * cache.page_size, add_scores)
-    return torch.empty(n, dtype=torch.uint8, device=cache.pool.device)
+    return cache.pool.new_empty(n)
 
 
 def qknorm_kv4_attention(cache, qkv, Hq, page_table, kv_lens, q_starts=None, max_q=1, scale=None,
@@ -246,43 +262,47 @@ def qknorm_kv4_attention(cache, qkv, Hq, page_table, kv_lens, q_starts=None, max
     cached row's weight to ``cache.scores``.  ``out`` and ``lse`` may be given;
     rows of no sequence are left as they are in them, and are undefined in
     outputs that are allocated here.  See include/qknorm_kv4.h."""
-    import torch
-
-    dev, D = cache.pool.device, cache.D
-    T, stride = _fused(qkv, "qkv", dev)
-    B = kv_lens.shape[0]
-    tp, t_stride, pages = _table(page_table, "page_table", B, dev)
-    lp = _vec(kv_lens, "kv_lens", torch.int32, B, dev)
-    qp = None if q_starts is None else _vec(q_starts, "q_starts", torch.int32, B + 1, dev)
-    if qkv.shape[1] < Hq * D:
+    index = cache.index
+    if stream is not None or _device_now() != index:
+        with _Elsewhere(cache.pool.device, stream):
+            return qknorm_kv4_attention(cache, qkv, Hq, page_table, kv_lens, q_starts, max_q,
+                                        scale, add_scores, out, lse, workspace)
+    D = cache.D
+    T, width, stride = _rows(qkv, "qkv", index)
+    if width < Hq * D:
         raise ValueError("qkv has fewer than Hq * D columns")
+    B = kv_lens.numel()
+    tp, t_stride, pages = _table(page_table, "page_table", B, index)
+    lp = _vec(kv_lens, "kv_lens", torch.int32, B, index)
+    qp = None if q_starts is None else _vec(q_starts, "q_starts", torch.int32, B + 1, index)
     if add_scores and cache.scores is None:
         raise ValueError("add_scores needs a cache with scores")
-    code = _dtype_code(qkv)
-    with _On(dev, stream):
-        if out is None:
-            out = torch.empty((T, Hq * D), dtype=qkv.dtype, device=dev)
-        elif out.dtype != qkv.dtype or out.shape != (T, Hq * D):
+    code = _code(qkv, "qkv")
+    out_stride = Hq * D
+    if out is None:
+        out = qkv.new_empty((T, out_stride))
+    else:
+        n, m, out_stride = _rows(out, "out", index)
+        if out.dtype is not qkv.dtype or n != T or m != Hq * D:
             raise ValueError("out must be [T, Hq * D] in qkv's type")
-        _, out_stride = _fused(out, "out", dev)
-        if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        elif (lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()
-              or lse.device != dev):
-            raise ValueError("lse must be a contiguous float32 tensor [T, Hq]")
-        if workspace is None:
-            workspace = torch.empty(_workspace_bytes(B, code, Hq, cache, max_q,
-                                                     pages * cache.page_size, add_scores),
-                                    dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous, on the cache's device")
-        rc = _lib().qknorm_kv4_attention(
-            qkv.data_ptr(), code, T, Hq, cache.Hk, D, stride, cache.pool.data_ptr(),
-            cache.num_pages, cache.page_size, tp, t_stride, pages, lp, B, qp, max_q,
-            D ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, lse.data_ptr(),
-            cache.scores.data_ptr() if add_scores else None, workspace.data_ptr(),
-            workspace.nbytes, _stream_of(dev))
-    _check("qknorm_kv4_attention", rc)
+    if lse is None:
+        lse = qkv.new_empty((T, Hq), dtype=torch.float32)
+    elif (lse.dtype is not torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous()
+          or lse.get_device() != index):
+        raise ValueError("lse must be a contiguous float32 tensor [T, Hq]")
+    if workspace is None:
+        workspace = cache.pool.new_empty(_workspace_bytes(
+            B, code, Hq, cache, max_q, pages * cache.page_size, add_scores))
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on the cache's device")
+    rc = (_kv4_lib or _lib()).qknorm_kv4_attention(
+        qkv.data_ptr(), code, T, Hq, cache.Hk, D, stride, cache._pool_ptr, cache.num_pages,
+        cache.page_size, tp, t_stride, pages, lp, B, qp, max_q,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, lse.data_ptr(),
+        cache._scores_ptr if add_scores else None, workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(index))
+    if rc:
+        _check("qknorm_kv4_attention", rc)
     return out, lse
 
 
@@ -292,23 +312,24 @@ def qknorm_kv4_evict(cache, page_table, kv_lens, dst_table, budget, recent, stre
     ``dst_table`` (int32 [B, pages]; none of them read).  Returns ``(new_lens
     int32 [B], kept int32 [B, Hk, budget])``, the kept rows' numbers with -1
     behind the last."""
-    import torch
-
-    dev = cache.pool.device
+    index = cache.index
+    if stream is not None or _device_now() != index:
+        with _Elsewhere(cache.pool.device, stream):
+            return qknorm_kv4_evict(cache, page_table, kv_lens, dst_table, budget, recent)
     if cache.scores is None:
         raise ValueError("eviction needs a cache with scores")
-    B = kv_lens.shape[0]
-    tp, t_stride, pages = _table(page_table, "page_table", B, dev)
-    dp, d_stride, d_pages = _table(dst_table, "dst_table", B, dev)
-    lp = _vec(kv_lens, "kv_lens", torch.int32, B, dev)
+    B = kv_lens.numel()
+    tp, t_stride, pages = _table(page_table, "page_table", B, index)
+    dp, d_stride, d_pages = _table(dst_table, "dst_table", B, index)
+    lp = _vec(kv_lens, "kv_lens", torch.int32, B, index)
     if not 1 <= budget <= d_pages * cache.page_size or not 0 <= recent <= budget:
         raise ValueError("1 <= budget <= dst_table's rows and 0 <= recent <= budget are required")
-    with _On(dev, stream):
-        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        kept = torch.empty((B, cache.Hk, budget), dtype=torch.int32, device=dev)
-        rc = _lib().qknorm_kv4_evict(
-            cache.pool.data_ptr(), cache.num_pages, cache.page_size, cache.Hk, cache.D,
-            cache.scores.data_ptr(), tp, t_stride, pages, lp, B, dp, d_stride, d_pages, budget,
-            recent, new_lens.data_ptr(), kept.data_ptr(), _stream_of(dev))
-    _check("qknorm_kv4_evict", rc)
+    new_lens = kv_lens.new_empty(B)
+    kept = kv_lens.new_empty((B, cache.Hk, budget))
+    rc = (_kv4_lib or _lib()).qknorm_kv4_evict(
+        cache._pool_ptr, cache.num_pages, cache.page_size, cache.Hk, cache.D, cache._scores_ptr,
+        tp, t_stride, pages, lp, B, dp, d_stride, d_pages, budget, recent, new_lens.data_ptr(),
+        kept.data_ptr(), _raw_stream(index))
+    if rc:
+        _check("qknorm_kv4_evict", rc)
     return new_lens, kept
