@@ -29,6 +29,16 @@
 
 namespace {
 
+// What a block of the attention kernel leaves for the kernels behind it: its
+// run of units, and the split item that begins in it (join_b < 0: none).
+struct RunRecord {
+    int64_t first, all;      // first unit, and all units of the call
+    int total;               // units of the run
+    int b, item, unit;       // where it begins
+    int join_b, join_item;   // the item
+    int join_slot, join_last;  // its part here, and the last block that holds one
+};
+
 struct AttentionArgs {
     const void *q;
     int64_t T, row_stride, out_stride;
@@ -48,6 +58,7 @@ struct AttentionArgs {
     int direct;        // one block per item, no item is split
     int max_items;     // items of a sequence at most (direct)
     int log_rows;      // query rows of a logit record
+    RunRecord *runs;   // [blocks]
     float *part;       // [2 * blocks][rows][D]: sums of items split over blocks
     float2 *part_ml;   // [2 * blocks][rows]: their maximum and sum
     float2 *row_ml;    // [B][max_q * Hq]: each query row's maximum and 1 / sum (scores)
@@ -314,6 +325,19 @@ __device__ __forceinline__ void store8(TS *p, const float (&f)[8])
                                                    f32_to_e4m3x4(f[4], f[5], f[6], f[7]));
     }
 }
+template <typename TS>
+__device__ __forceinline__ void store4(TS *p, float x, float y, float z, float w)
+{
+    if constexpr (sizeof(TS) == 4) {
+        *reinterpret_cast<float4 *>(p) = make_float4(x, y, z, w);
+    } else if constexpr (sizeof(TS) == 2) {
+        const float f[8] = {x, y, z, w};
+        const uint4 u = Storage<TS>::pack(f);
+        *reinterpret_cast<uint2 *>(p) = make_uint2(u.x, u.y);
+    } else {
+        *reinterpret_cast<uint32_t *>(p) = f32_to_e4m3x4(x, y, z, w);
+    }
+}
 // Elements (p, p + 4) as an operand register, part by part; odd pairs meet
 // raw codes that are 16 times too large.
 template <typename TS>
@@ -344,8 +368,8 @@ constexpr int kUnitBytes = 2 * kBlockBytes<D>;
 template <int D>
 constexpr int kStages = D == 64 ? 3 : 2;
 template <int D, int NT>
-constexpr int kAttentionSmem = kWarps * kStages<D> * kUnitBytes<D> + 8 * NT * (D + 4) * 4 +
-                               3 * kWarps * 8 * NT * 4;
+constexpr int kAttentionSmem = kWarps * (kStages<D> * kUnitBytes<D> + 8 * NT * (D + 4) * 4 +
+                                         8 * NT * 16);
 
 // A weight is held as p * 2^kWeightExp * (scale_v / vref), p relative to a
 // maximum that may lag behind by 2^kLag, so that it is rarely moved: at most
@@ -380,9 +404,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
     const int g = lane / 4, t = lane % 4;
     uint8_t *ring = smem + warp * kS * kUnitBytes<D>;
     float *join = reinterpret_cast<float *>(smem + kWarps * kS * kUnitBytes<D>);
-    float *join_m = join + kR * (D + 4);
-    float *join_l = join_m + kWarps * kR;
-    float *join_z = join_l + kWarps * kR;
+    float4 *join_m = reinterpret_cast<float4 *>(join + kWarps * kR * (D + 4));
     pdl_wait_then_release();
 
     Walk<kR> w;
@@ -396,7 +418,11 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
         if (w.item >= w.items) return;
         total = w.units;
     } else {
-        block_run<kR>(a, scan, w, first, total);
+        const int64_t all = block_run<kR>(a, scan, w, first, total);
+        if (tid == 0) {
+            RunRecord rec = {first, all, total, w.b, w.item, w.unit, -1, 0, 0, 0};
+            a.runs[blockIdx.x] = rec;
+        }
         if (total <= 0) return;
     }
 
@@ -469,64 +495,62 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
         const int seg_units = min(w.units - w.unit, total - at);
         const bool whole = w.unit == 0 && seg_units == w.units;
 
-        // The query operand, and what each of the lane's columns needs.  Two
-        // passes over the rows: the largest element, then the operand.
+        // The query operand, and what each of the lane's columns needs.
         uint32_t qf[NT][kQP][kKSteps][2];
         float qsum[NT][2];
         int vis[NT][2];
         int all_see = seq.n;
         const float c2 = a.scale * 1.4426950408889634f;
-        float largest = 0.f, factor = 1.f;
+        float largest = 0.f;
+        const TS *src[NT];
+        bool live[NT];
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + g;
+            live[nt] = r < rows;
+            const int qr = live[nt] ? tile * kR + r : 0;
+            const int i = qr / a.group;
+            src[nt] = static_cast<const TS *>(a.q) + (int64_t)(seq.start + i) * a.row_stride +
+                      (int64_t)(hk * a.group + qr - i * a.group) * D + t * (D / 4);
+            const int v = live[nt] ? seq.n - seq.count + i + 1 : seq.n;
+            all_see = min(all_see, v);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int r = nt * 8 + g;
-                const bool live = r < rows;
-                const int qr = live ? tile * kR + r : 0;
-                const int i = qr / a.group;
-                const TS *src = static_cast<const TS *>(a.q) +
-                                (int64_t)(seq.start + i) * a.row_stride +
-                                (int64_t)(hk * a.group + qr - i * a.group) * D + t * (D / 4);
-                float s = 0.f;
+            for (int e = 0; e < 2; ++e) vis[nt][e] = __shfl_sync(0xffffffffu, v, (2 * t + e) * 4);
 #pragma unroll
-                for (int ww = 0; ww < kKWords; ++ww) {
-                    float f[8] = {};
-                    if (live) load8(src + ww * 8, f);
-                    if (pass == 0) {
+            for (int ww = 0; ww < kKWords; ++ww) {
+                float f[8] = {};
+                if (live[nt]) load8(src[nt] + ww * 8, f);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (fabsf(f[e]) <= 3.402823466e38f) largest = fmaxf(largest, fabsf(f[e]));
-                    } else {
-                        uint32_t pairs[kQP][4];
-                        query_pairs<TS>(f, factor, pairs);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) s += f[e];
-#pragma unroll
-                        for (int part = 0; part < kQP; ++part)
-#pragma unroll
-                            for (int p = 0; p < 4; ++p)
-                                qf[nt][part][ww * 2 + p / 2][p % 2] = pairs[part][p];
-                    }
-                }
-                if (pass == 0) continue;
-                s += __shfl_xor_sync(0xffffffffu, s, 1);
-                s += __shfl_xor_sync(0xffffffffu, s, 2);
-                s *= c2;
-                const int v = live ? seq.n - seq.count + i + 1 : seq.n;
-                all_see = min(all_see, v);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    qsum[nt][e] = __shfl_sync(0xffffffffu, s, (2 * t + e) * 4);
-                    vis[nt][e] = __shfl_sync(0xffffffffu, v, (2 * t + e) * 4);
-                }
+                for (int e = 0; e < 8; ++e)
+                    if (fabsf(f[e]) <= 3.402823466e38f) largest = fmaxf(largest, fabsf(f[e]));
             }
-            if (pass == 0) {
+        }
 #pragma unroll
-                for (int o = 1; o < 32; o *= 2)
-                    largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, o));
-                factor = power_of_two(min(max(kQueryExp - exponent_of(largest), -103), 113));
+        for (int o = 1; o < 32; o *= 2)
+            largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+        const float factor = power_of_two(min(max(kQueryExp - exponent_of(largest), -103), 113));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float s = 0.f;
+#pragma unroll
+            for (int ww = 0; ww < kKWords; ++ww) {  // again, from L1
+                float f[8] = {};
+                if (live[nt]) load8(src[nt] + ww * 8, f);
+                uint32_t pairs[kQP][4];
+                query_pairs<TS>(f, factor, pairs);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += f[e];
+#pragma unroll
+                for (int part = 0; part < kQP; ++part)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        qf[nt][part][ww * 2 + p / 2][p % 2] = pairs[part][p];
             }
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            s *= c2;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) qsum[nt][e] = __shfl_sync(0xffffffffu, s, (2 * t + e) * 4);
         }
 #pragma unroll
         for (int o = 4; o < 32; o *= 2)
@@ -755,12 +779,16 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                             for (int part = 0; part < kWP; ++part) {
                                 const uint32_t b0 = wf[half][nt][part][0], b1 = wf[half][nt][part][1];
                                 mma(acc[4 * v + p][nt], x0[p], x1[p], x2[p], x3[p], b0, b1);
-                                if constexpr (kRawV) {
-                                    // -8, as large as the tile's raw codes are.
-                                    const uint32_t c = p % 2 ? 0x80808080u : 0x80088008u;
-                                    mma(acc[4 * v + p][nt], c, c, c, c, b0, b1);
-                                }
                             }
+                    if constexpr (kRawV) {
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            // -8, as large as the tile's raw codes are.
+                            const uint32_t c = p % 2 ? 0x80808080u : 0x80088008u;
+                            mma(acc[4 * v + p][0], c, c, c, c, wf[half][0][0][0],
+                                wf[half][0][0][1]);
+                        }
+                    }
                 }
             }
         };
@@ -779,79 +807,61 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
             stage = stage + 1 == kS ? 0 : stage + 1;
         }
 
-        // Join the four warps, in order.
+        // Each warp's sums, maxima and vref meet in shared memory.
+        {
+            // The sums' own power of two (odd tiles of raw codes: 16 times less).
+            constexpr float kEven = (kRawV ? 16777216.f : 1.f) / (1 << kWeightExp);
+            constexpr float kOdd = kRawV ? kEven / 16.f : kEven;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < 2; ++e) {
+                    const int col = nt * 8 + 2 * t + e;
+                    float *to = join + (warp * kR + col) * (D + 4) + g * (D / 8);
 #pragma unroll
-                for (int o = 4; o < 32; o *= 2) {
-                    l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
-                    z[nt][e] += __shfl_xor_sync(0xffffffffu, z[nt][e], o);
-                }
-                if (g == 0) {
-                    const int i = warp * kR + nt * 8 + 2 * t + e;
-                    join_m[i] = m[nt][e];
-                    join_l[i] = l[nt][e];
-                    join_z[i] = z[nt][e];
-                }
-            }
-        __syncthreads();
-        float f[NT][2];
+                    for (int v = 0; v < kVWords; ++v)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+                        for (int hi = 0; hi < 2; ++hi) {
+                            const int c = 2 * hi + e;
+                            *reinterpret_cast<float4 *>(to + v * 8 + hi * 4) = make_float4(
+                                acc[4 * v][nt][c] * kEven, acc[4 * v + 1][nt][c] * kOdd,
+                                acc[4 * v + 2][nt][c] * kEven, acc[4 * v + 3][nt][c] * kOdd);
+                        }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int col = nt * 8 + 2 * t + e;
-                float mm = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, join_m[i * kR + col]);
-                f[nt][e] = mm == -INFINITY ? 0.f : exp2_approx(m[nt][e] - mm) * vref;
-            }
-        for (int i = 0; i < kWarps; ++i) {
-            if (warp == i) {
-                // The sums' own power of two (odd tiles of raw codes: 16 times less).
-                constexpr float kEven = (kRawV ? 16777216.f : 1.f) / (1 << kWeightExp);
-                constexpr float kOdd = kRawV ? kEven / 16.f : kEven;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float *to = join + (nt * 8 + 2 * t + e) * (D + 4) + g * (D / 8);
-                        const float by = f[nt][e];
-#pragma unroll
-                        for (int v = 0; v < kVWords; ++v)
-#pragma unroll
-                            for (int hi = 0; hi < 2; ++hi) {
-                                float4 *p = reinterpret_cast<float4 *>(to + v * 8 + hi * 4);
-                                float4 x = i > 0 ? *p : make_float4(0.f, 0.f, 0.f, 0.f);
-                                const int c = 2 * hi + e;
-                                x.x = fmaf(acc[4 * v][nt][c] * kEven, by, x.x);
-                                x.y = fmaf(acc[4 * v + 1][nt][c] * kOdd, by, x.y);
-                                x.z = fmaf(acc[4 * v + 2][nt][c] * kEven, by, x.z);
-                                x.w = fmaf(acc[4 * v + 3][nt][c] * kOdd, by, x.w);
-                                *p = x;
-                            }
+                    for (int o = 4; o < 32; o *= 2) {
+                        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
+                        z[nt][e] += __shfl_xor_sync(0xffffffffu, z[nt][e], o);
                     }
-            }
-            __syncthreads();
+                    if (g == 0)
+                        join_m[warp * kR + col] = make_float4(m[nt][e], l[nt][e], z[nt][e], vref);
+                }
         }
-        // Eight elements of a row to a thread.
+        __syncthreads();
+        // Eight elements of a row to a thread; the warps are added in order.
         const int slot = 2 * blockIdx.x + (seg_index > 0 ? 1 : 0);
         for (int i = tid; i < rows * (D / 8); i += kThreads) {
             const int r = i / (D / 8), d = (i % (D / 8)) * 8;
+            float4 mlz[kWarps];
             float mm = -INFINITY, ll = 0.f, zz = 0.f;
 #pragma unroll
-            for (int v = 0; v < kWarps; ++v) mm = fmaxf(mm, join_m[v * kR + r]);
+            for (int v = 0; v < kWarps; ++v) {
+                mlz[v] = join_m[v * kR + r];
+                mm = fmaxf(mm, mlz[v].x);
+            }
+            float o[8] = {};
 #pragma unroll
             for (int v = 0; v < kWarps; ++v) {
-                const float e = mm == -INFINITY ? 0.f : exp2_approx(join_m[v * kR + r] - mm);
-                ll = fmaf(join_l[v * kR + r], e, ll);
-                zz = fmaf(join_z[v * kR + r], e, zz);
-            }
-            float o[8];
+                const float e = mm == -INFINITY ? 0.f : exp2_approx(mlz[v].x - mm);
+                ll = fmaf(mlz[v].y, e, ll);
+                zz = fmaf(mlz[v].z, e, zz);
+                const float ev = e * mlz[v].w;
+                float x[8];
+                load8(join + (v * kR + r) * (D + 4) + d, x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = join[r * (D + 4) + d + e] + zz;
+                for (int k = 0; k < 8; ++k) o[k] = fmaf(x[k], ev, o[k]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] += zz;
             if (whole) {
                 const float inv = ll == 0.f ? 0.f : 1.f / ll;
 #pragma unroll
@@ -875,6 +885,16 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                 if (d == 0) a.part_ml[(int64_t)slot * kR + r] = make_float2(mm, ll);
             }
         }
+        if (tid == 0 && w.unit == 0 && !whole) {
+            // The item goes on in the blocks behind this one.
+            RunRecord &rec = a.runs[blockIdx.x];
+            const int64_t all = rec.all, last_unit = first + at + w.units - 1;
+            const int64_t blocks = all < gridDim.x ? all : gridDim.x;
+            rec.join_b = w.b;
+            rec.join_item = w.item;
+            rec.join_slot = slot;
+            rec.join_last = (int)(((last_unit + 1) * blocks - 1) / all);
+        }
         __syncthreads();
         at += seg_units;
         seg_index = 1;
@@ -883,123 +903,172 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
     cp_async_wait<0>();
 }
 
-// Joins the items whose units were split over blocks: one warp to a query
-// row, the parts added in the blocks' order.
+// Joins the items whose units were split over blocks, the parts added in the
+// blocks' order: block x joins the item that begins in the attention kernel's
+// block x and goes on behind it, two query rows to a block.  D/4 threads hold a
+// row, four elements each, and the block's other threads take every kGroups-th
+// part of the same rows.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 2;
 template <typename TS, int D, int kR, bool kScores>
-__global__ void __launch_bounds__(kThreads)
-qkn_kv4_join_kernel(const AttentionArgs a)
+__global__ void __launch_bounds__(kJoinThreads) qkn_kv4_join_kernel(const AttentionArgs a)
 {
-    constexpr int kE = D / 32;
-    __shared__ int64_t scan[kWarps + 2];
+    constexpr int kLanes = kJoinRows * D / 4;
+    constexpr int kGroups = kJoinThreads / kLanes;
+    __shared__ float4 sums[kJoinThreads];
+    __shared__ float total[kGroups][kJoinRows], most[kJoinThreads / 32][kJoinRows];
     pdl_wait_then_release();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    // The parts of a block are those of its run's first and last items; each
-    // split item is joined by the block that holds its first unit, which
-    // finds it as the last item of its run.
-    Walk<kR> w;
-    int64_t first;
-    int total;
-    const int64_t all = block_run<kR>(a, scan, w, first, total);
-    if (total <= 0) return;
-    int slot = 2 * blockIdx.x;
-    int left = total;  // units from w on
-    while (left > w.units - w.unit) {
-        left -= w.units - w.unit;
-        // Skip whole items of the same sequence in one step.
-        w.unit = 0;
-        if (++w.item >= w.items) {
-            w.item = 0;
-            do {
-                ++w.b;
-                w.load(a);
-            } while (w.items == 0);
-        }
-        const int more = min(w.items - 1 - w.item, (left - 1) / w.units);
-        w.item += more;
-        left -= more * w.units;
-        slot = 2 * blockIdx.x + 1;
-    }
-    // The last item of the run: does it begin here, and go on in later blocks?
-    if (w.unit != 0 || left == w.units) return;
-    const int64_t last_unit = first + total - left + w.units - 1;
-    const int64_t blocks = all < gridDim.x ? all : gridDim.x;
-    const int last = (int)(((last_unit + 1) * blocks - 1) / all);
-    const Seq seq = load_seq<kR>(a, w.b);
-    const int hk = w.item % a.pool.Hk, tile = w.item / a.pool.Hk;
+    const RunRecord rec = a.runs[blockIdx.x];
+    if (rec.join_b < 0) return;
+    const Seq seq = load_seq<kR>(a, rec.join_b);
+    const int hk = rec.join_item % a.pool.Hk, tile = rec.join_item / a.pool.Hk;
     const int rows = min(kR, seq.count * a.group - tile * kR);
-    for (int r = warp; r < rows; r += kWarps) {
-        float mm = -INFINITY;
-        for (int c = blockIdx.x + lane; c <= last; c += 32)
-            mm = fmaxf(mm, a.part_ml[(int64_t)(c == blockIdx.x ? slot : 2 * c) * kR + r].x);
+    const int r0 = blockIdx.y * kJoinRows;
+    if (r0 >= rows) return;
+    const int tid = threadIdx.x, parts = rec.join_last - (int)blockIdx.x + 1;
+    const auto at = [&](int c, int r) {  // part c's row r
+        return (int64_t)(c == 0 ? rec.join_slot : 2 * (blockIdx.x + c)) * kR + r0 + r;
+    };
+    float m0 = -INFINITY, m1 = -INFINITY;
+    for (int c = tid; c < parts; c += kJoinThreads) {
+        m0 = fmaxf(m0, a.part_ml[at(c, 0)].x);
+        m1 = fmaxf(m1, a.part_ml[at(c, 1)].x);
+    }
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-        float o[kE] = {}, ll = 0.f;
-        for (int c = blockIdx.x; c <= last; ++c) {
-            const int64_t at = (int64_t)(c == (int)blockIdx.x ? slot : 2 * c) * kR + r;
-            const float2 ml = a.part_ml[at];
-            const float e = mm == -INFINITY ? 0.f : exp2_approx(ml.x - mm);
-            ll = fmaf(ml.y, e, ll);
+    for (int o = 16; o > 0; o /= 2) {
+        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    }
+    if (tid % 32 == 0) {
+        most[tid / 32][0] = m0;
+        most[tid / 32][1] = m1;
+    }
+    __syncthreads();
+    const int group = tid / kLanes, r = tid % kLanes / (D / 4), d = tid % (D / 4) * 4;
+    float mm = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kE; ++i) o[i] = fmaf(a.part[at * D + lane * kE + i], e, o[i]);
-        }
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        const int qr = tile * kR + r;
-        const int qi = qr / a.group, h = hk * a.group + qr - qi * a.group;
-        TS *to = static_cast<TS *>(a.out) + (int64_t)(seq.start + qi) * a.out_stride +
-                 (int64_t)h * D + lane * kE;
+    for (int i = 0; i < kJoinThreads / 32; ++i) mm = fmaxf(mm, most[i][r]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float ll = 0.f;
+#pragma unroll 4
+    for (int c = group; c < parts; c += kGroups) {
+        const float2 ml = a.part_ml[at(c, r)];
+        const float4 x = *reinterpret_cast<const float4 *>(a.part + at(c, r) * D + d);
+        const float e = mm == -INFINITY ? 0.f : exp2_approx(ml.x - mm);
+        ll = fmaf(ml.y, e, ll);
+        o.x = fmaf(x.x, e, o.x);
+        o.y = fmaf(x.y, e, o.y);
+        o.z = fmaf(x.z, e, o.z);
+        o.w = fmaf(x.w, e, o.w);
+    }
+    sums[tid] = o;
+    if (d == 0) total[group][r] = ll;
+    __syncthreads();
+    if (group > 0 || r0 + r >= rows) return;
+    ll = total[0][r];
 #pragma unroll
-        for (int i = 0; i < kE; ++i) to[i] = (TS)(ll == 0.f ? 0.f : o[i] * inv);
-        if (lane == 0) {
-            if (a.lse != nullptr)
-                a.lse[(int64_t)(seq.start + qi) * a.Hq + h] =
-                    ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
-            if constexpr (kScores)
-                a.row_ml[(int64_t)w.b * a.max_q * a.Hq + qi * a.Hq + h] =
-                    make_float2(ll == 0.f ? 0.f : mm, inv);
-        }
+    for (int i = 1; i < kGroups; ++i) {
+        const float4 x = sums[tid + i * kLanes];
+        o.x += x.x;
+        o.y += x.y;
+        o.z += x.z;
+        o.w += x.w;
+        ll += total[i][r];
+    }
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const int qr = tile * kR + r0 + r;
+    const int qi = qr / a.group, h = hk * a.group + qr - qi * a.group;
+    TS *to = static_cast<TS *>(a.out) + (int64_t)(seq.start + qi) * a.out_stride + (int64_t)h * D + d;
+    const bool none = ll == 0.f;
+    store4(to, none ? 0.f : o.x * inv, none ? 0.f : o.y * inv, none ? 0.f : o.z * inv,
+           none ? 0.f : o.w * inv);
+    if (d == 0) {
+        if (a.lse != nullptr)
+            a.lse[(int64_t)(seq.start + qi) * a.Hq + h] =
+                none ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+        if constexpr (kScores)
+            a.row_ml[(int64_t)rec.join_b * a.max_q * a.Hq + qi * a.Hq + h] =
+                make_float2(none ? 0.f : mm, inv);
     }
 }
 
-// Adds each cached row's weight to its score: a warp to a unit, a lane to a
-// row, over all the items of the unit's key/value head.
+// Adds each cached row's weight to its score: a lane to a row, over all the
+// items of its key/value head (whose logits lie tile_units apart), a warp to
+// kBatch units in a row, so that their loads are in flight together.
+constexpr int kScoreThreads = 256;
+constexpr int kScoreSplit = 2;  // blocks to a run
 template <int kR>
-__global__ void __launch_bounds__(kThreads) qkn_kv4_scores_kernel(const AttentionArgs a)
+__global__ void __launch_bounds__(kScoreThreads) qkn_kv4_scores_kernel(const AttentionArgs a)
 {
-    __shared__ int64_t scan[kWarps + 2];
+    constexpr int kBatch = 4;
+    constexpr int kStep = kScoreThreads / 32 * kScoreSplit;
     pdl_wait_then_release();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const RunRecord rec = a.runs[blockIdx.x];
+    const int lane = threadIdx.x % 32;
+    const int mine = blockIdx.y * (kScoreThreads / 32) + threadIdx.x / 32;
     Walk<kR> w;
-    int64_t first;
-    int total;
-    block_run<kR>(a, scan, w, first, total);
-    for (int k = 0; k < total; ++k) {
-        // The units of a head's first tile stand for the head.
-        if (w.item < a.pool.Hk && (k % kWarps) == warp) {
+    w.b = rec.b;
+    w.item = rec.item;
+    w.unit = rec.unit;
+    if (rec.total > 0) w.load(a);
+    // Batches of the run, item by item; every kStep-th is this warp's.
+    int k = 0, batch = 0;
+    while (k < rec.total) {
+        const int left = min(w.units - w.unit, rec.total - k);
+        const int batches = (left + kBatch - 1) / kBatch;
+        // Only a head's first tile stands for its units.
+        if (w.item < a.pool.Hk) {
             const Seq seq = load_seq<kR>(a, w.b);
-            const int hk = w.item;
-            const int j = w.unit * kUnitRows + lane;
-            if (j < seq.n) {
-                const int64_t page =
-                    a.page_table[w.b * a.table_stride + (j >> a.pool.log2_page)];
-                if (page_ok(a.pool, page)) {
-                    float add = 0.f;
-                    const int64_t tile_units = (int64_t)a.pool.Hk * w.units;
-                    const float *x = a.logits + ((first + k) * kUnitRows + lane) * a.log_rows;
-                    const float2 *ml = a.row_ml + (int64_t)w.b * a.max_q * a.Hq;
-                    const int rows = seq.count * a.group;
-                    for (int r = 0; r < rows; ++r) {
-                        const int qi = r / a.group, h = hk * a.group + r - qi * a.group;
-                        const float2 f = ml[qi * a.Hq + h];
-                        const float v =
-                            x[(int64_t)(r / kR) * tile_units * kUnitRows * a.log_rows + r % kR];
-                        add = fmaf(exp2_approx(v - f.x), f.y, add);
+            const int hk = w.item, rows = seq.count * a.group;
+            const int64_t tile_stride = (int64_t)a.pool.Hk * w.units * kUnitRows * a.log_rows;
+            const float2 *ml = a.row_ml + (int64_t)w.b * a.max_q * a.Hq + hk * a.group;
+            const int32_t *table = a.page_table + w.b * a.table_stride;
+            int i = mine - batch % kStep;
+            if (i < 0) i += kStep;
+            for (; i < batches; i += kStep) {
+                const int u = i * kBatch;
+                int64_t at[kBatch];
+                float add[kBatch] = {}, old[kBatch];
+                const float *x = a.logits + ((rec.first + k + u) * kUnitRows + lane) * a.log_rows;
+#pragma unroll
+                for (int v = 0; v < kBatch; ++v) {
+                    const int j = (w.unit + u + v) * kUnitRows + lane;
+                    at[v] = -1;
+                    if (u + v < left && j < seq.n) {
+                        const int64_t page = table[j >> a.pool.log2_page];
+                        if (page_ok(a.pool, page))
+                            at[v] = ((page * a.pool.Hk + hk) << a.pool.log2_page) +
+                                    (j & ((1 << a.pool.log2_page) - 1));
                     }
-                    const int off = j & ((1 << a.pool.log2_page) - 1);
-                    a.scores[((page * a.pool.Hk + hk) << a.pool.log2_page) + off] += add;
                 }
+#pragma unroll
+                for (int v = 0; v < kBatch; ++v) old[v] = at[v] >= 0 ? a.scores[at[v]] : 0.f;
+                for (int tile = 0, r = 0; r < rows; ++tile) {
+                    const float *xt = x + tile * tile_stride;
+                    for (const int end = min(rows, r + kR); r < end; r += 2) {
+                        const int qi = r / a.group, qj = (r + 1) / a.group;
+                        const bool two = r + 1 < rows;
+                        const float2 f = ml[qi * a.Hq + r - qi * a.group];
+                        const float2 f1 =
+                            two ? ml[qj * a.Hq + r + 1 - qj * a.group] : make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int v = 0; v < kBatch; ++v) {
+                            if (at[v] < 0) continue;
+                            const float2 y = *reinterpret_cast<const float2 *>(
+                                xt + v * kUnitRows * a.log_rows + r % kR);
+                            add[v] = fmaf(exp2_approx(y.x - f.x), f.y, add[v]);
+                            if (two) add[v] = fmaf(exp2_approx(y.y - f1.x), f1.y, add[v]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < kBatch; ++v)
+                    if (at[v] >= 0) a.scores[at[v]] = old[v] + add[v];
             }
+            batch += batches;
         }
-        if (k + 1 < total) w.step(a, 1);
+        k += left;
+        if (k < rec.total) w.step(a, left);
     }
 }
 

@@ -193,7 +193,7 @@ struct AttentionPlan {
     int nt, log_rows, max_items;
     bool direct;
     int64_t max_units;  // of an item
-    int64_t part, part_ml, row_ml, logits, bytes;  // offsets in the workspace, and its size
+    int64_t runs, part, part_ml, row_ml, logits, bytes;  // offsets in the workspace, and its size
 };
 
 AttentionPlan attention_plan(int64_t B, int dtype, int Hq, int Hk, int D, int max_q,
@@ -210,7 +210,9 @@ AttentionPlan attention_plan(int64_t B, int dtype, int Hq, int Hk, int D, int ma
     p.log_rows = (int)(rows < kr ? (rows + 1) / 2 * 2 : kr);
     // Sizes may pass 63 bits for arguments that no buffer could have.
     __int128 at = 0;
-    p.part = 0;
+    p.runs = 0;
+    at += kMaxBlocks * sizeof(RunRecord);
+    p.part = (int64_t)at;
     at += (__int128)2 * kMaxBlocks * kr * D * 4;
     p.part_ml = (int64_t)at;
     at += (__int128)2 * kMaxBlocks * kr * 8;
@@ -263,9 +265,11 @@ int launch_attention(const AttentionArgs &a, const AttentionPlan &p, cudaStream_
     if (grid > units) grid = units;
     const dim3 blocks((unsigned)grid);
     if ((rc = launch(kern, blocks, kThreads, smem, stream, a)) != QKN_OK) return rc;
-    rc = launch(qkn_kv4_join_kernel<TS, D, 8 * NT, kScores>, blocks, kThreads, 0, stream, a);
+    rc = launch(qkn_kv4_join_kernel<TS, D, 8 * NT, kScores>,
+                dim3((unsigned)grid, 8 * NT / kJoinRows), kJoinThreads, 0, stream, a);
     if (rc != QKN_OK || !kScores) return rc;
-    return launch(qkn_kv4_scores_kernel<8 * NT>, blocks, kThreads, 0, stream, a);
+    return launch(qkn_kv4_scores_kernel<8 * NT>, dim3((unsigned)grid, kScoreSplit), kScoreThreads,
+                  0, stream, a);
 }
 
 struct Attention {
@@ -401,6 +405,7 @@ int qknorm_kv4_attention(const void *q, int dtype, int64_t T, int Hq, int Hk, in
     a.max_items = plan.max_items;
     a.log_rows = plan.log_rows;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    a.runs = reinterpret_cast<RunRecord *>(ws + plan.runs);
     a.part = reinterpret_cast<float *>(ws + plan.part);
     a.part_ml = reinterpret_cast<float2 *>(ws + plan.part_ml);
     a.row_ml = reinterpret_cast<float2 *>(ws + plan.row_ml);
