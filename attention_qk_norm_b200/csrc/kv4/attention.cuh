@@ -91,9 +91,13 @@ __device__ __forceinline__ void q_range(const AttentionArgs &a, int b, int &star
 // sequence with up to kR of its query rows.  Units are numbered sequence by
 // sequence, item by item, and the blocks take equal runs of them, whatever
 // the lengths are: lengths are device data, and a batch of mixed lengths
-// splits as evenly as one of equal ones.  An item with no cached row still
-// has one (empty) unit, which writes its outputs.
+// splits as evenly as one of equal ones.  Every item counts kItemUnits empty
+// units behind its own, the time that a block spends on an item beside its
+// units (measured on B200: without them a block with many short items came
+// last by 20 us of 97 for 64 sequences of 37 to 8192 rows); a run that would
+// end among them ends behind them.
 constexpr int kUnitRows = 32;
+constexpr int kItemUnits = 4;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 
@@ -109,7 +113,7 @@ __device__ __forceinline__ Seq load_seq(const AttentionArgs &a, int b)
     q_range(a, b, s.start, s.count);
     const int64_t rows = (int64_t)s.count * a.group;
     s.items = (int)((rows + kR - 1) / kR) * a.pool.Hk;
-    s.units = s.n > 0 ? (s.n + kUnitRows - 1) / kUnitRows : 1;
+    s.units = (s.n + kUnitRows - 1) / kUnitRows + kItemUnits;
     return s;
 }
 
@@ -171,33 +175,55 @@ __device__ __forceinline__ int64_t block_run(const AttentionArgs &a, int64_t *sc
         total += scan[i];
     }
     before += sum - mine;
-    // At most as many blocks as units take part, so that each has one.
+    // The run's two ends: scan[4..5] the sequence of the first and the units
+    // before it, scan[6..7] the ends, moved behind the empty units of the item
+    // that they fall among.
+    // At most as many blocks as units take part.
     const int64_t blocks = total < gridDim.x ? total : gridDim.x;
-    if (blockIdx.x < blocks) {
-        first = total * blockIdx.x / blocks;
-        count = (int)(total * (blockIdx.x + 1) / blocks - first);
-    } else {
-        first = count = 0;
-    }
-    if (count > 0 && first >= before && first < before + mine) {
-        int b = b0;
-        for (;; ++b) {  // ends: `first` lies in one of this thread's sequences
-            const Seq s = load_seq<kR>(a, b);
-            const int64_t u = (int64_t)s.items * s.units;
-            if (first < before + u) break;
-            before += u;
+    const bool part = blockIdx.x < blocks;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const int64_t at = part ? total * (blockIdx.x + side) / blocks : total;
+        if (at >= before && at < before + mine) {
+            int64_t seen = before;
+            int b = b0;
+            Seq s = load_seq<kR>(a, b);
+            for (;; s = load_seq<kR>(a, ++b)) {  // ends: `at` lies in one of these sequences
+                const int64_t u = (int64_t)s.items * s.units;
+                if (at < seen + u) break;
+                seen += u;
+            }
+            const int64_t in = at - seen;
+            const int64_t item = (uint32_t)(in >> 32) == 0 ? (uint32_t)in / (uint32_t)s.units
+                                                           : in / s.units;
+            const int unit = (int)(in - item * s.units);
+            const bool move = unit >= s.units - kItemUnits && unit > 0;
+            scan[6 + side] = move ? at + s.units - unit : at;
+            if (side == 0) {
+                scan[4] = b;
+                scan[5] = seen;
+            }
+        } else if (at == total && tid == 0) {
+            scan[6 + side] = total;
         }
-        scan[kWarps] = b;
-        scan[kWarps + 1] = before;
     }
     __syncthreads();
+    first = scan[6];
+    count = (int)(scan[7] - first);
     w.b = 0;
     if (count <= 0) return total;
-    w.b = (int)scan[kWarps];
+    w.b = (int)scan[4];
     w.load(a);
-    const int64_t in = first - scan[kWarps + 1];
-    w.item = (int)(in / w.units);
+    const int64_t in = first - scan[5];
+    w.item = (uint32_t)(in >> 32) == 0 ? (uint32_t)in / (uint32_t)w.units : (int)(in / w.units);
     w.unit = (int)(in - (int64_t)w.item * w.units);
+    if (w.item >= w.items) {  // moved behind the sequence's last item
+        w.item = 0;
+        do {
+            ++w.b;
+            w.load(a);
+        } while (w.items == 0);
+    }
     return total;
 }
 
@@ -399,7 +425,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
     constexpr int kChunks = kBB / 16;
 
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int64_t scan[kWarps + 2];
+    __shared__ int64_t scan[8];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int g = lane / 4, t = lane % 4;
     uint8_t *ring = smem + warp * kS * kUnitBytes<D>;
@@ -416,7 +442,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
         w.unit = 0;
         w.load(a);
         if (w.item >= w.items) return;
-        total = w.units;
+        total = w.units - kItemUnits > 0 ? w.units - kItemUnits : 1;
     } else {
         const int64_t all = block_run<kR>(a, scan, w, first, total);
         if (tid == 0) {
@@ -493,7 +519,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
         const int hk = w.item % a.pool.Hk, tile = w.item / a.pool.Hk;
         const int rows = min(kR, seq.count * a.group - tile * kR);  // live query rows
         const int seg_units = min(w.units - w.unit, total - at);
-        const bool whole = w.unit == 0 && seg_units == w.units;
+        const bool whole = w.unit == 0 && seg_units >= w.units - kItemUnits;
 
         // The query operand, and what each of the lane's columns needs.
         uint32_t qf[NT][kQP][kKSteps][2];
@@ -564,9 +590,8 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY;
 
-        // One unit; kMask: some of its rows are hidden from some of the queries.
-        auto consume = [&](auto mask_tag, const int k) {
-            constexpr bool kMask = decltype(mask_tag)::value;
+        // One unit.
+        auto consume = [&](const int k) {
             const uint8_t *unit = ring + stage * kUnitBytes<D>;
             const int base = (w.unit + k) * kUnitRows;
 
@@ -614,41 +639,61 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                 }
             }
 
-            // Logits in base 2, and the lane's largest.
+            // Logits in base 2.
             float vs[2][2], vm[2][2];
-            const uint32_t bad_here = kMask ? (bad >> (2 * stage)) & 3u : 0u;
-            float top[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
-            float vtop = 0.f;
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int row = row_of(g) + 8 * r;
-                    const uint8_t *par = unit + half * kBB + 16 * D + row * 4;
+                    const uint8_t *par = unit + half * kBB + 16 * D + (row_of(g) + 8 * r) * 4;
                     float ks, km;
                     unpack_params(*reinterpret_cast<const uint32_t *>(par), ks, km);
                     unpack_params(*reinterpret_cast<const uint32_t *>(par + 64), vs[half][r],
                                   vm[half][r]);
                     if constexpr (kRawK) km = fmaf(-8.f, ks, km);
                     ks *= c_s;
-                    const int j = base + half * kBlockRows + row;
-                    const bool gone = kMask && (j >= seq.n || (bad_here >> half & 1u));
-                    if (gone) vs[half][r] = vm[half][r] = 0.f;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            s[half][nt][2 * r + e] =
+                                fmaf(ks, s[half][nt][2 * r + e], km * qsum[nt][e]);
+                }
+            // Rows that are hidden from some of the queries, or from all.
+            const uint32_t bad_here = (bad >> (2 * stage)) & 3u;
+            const bool masked = base + kUnitRows > all_see || bad_here != 0;
+            if (masked) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int j = base + half * kBlockRows + row_of(g) + 8 * r;
+                        const bool gone = j >= seq.n || (bad_here >> half & 1u);
+                        if (gone) vs[half][r] = vm[half][r] = 0.f;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (gone || j >= vis[nt][e]) s[half][nt][2 * r + e] = -INFINITY;
+                    }
+            }
+            // The lane's largest.
+            float vtop = 0.f, top[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
                     vtop = fmaxf(vtop, vs[half][r]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float &x = s[half][nt][2 * r + e];
-                            x = fmaf(ks, x, km * qsum[nt][e]);
-                            if (kMask && (gone || j >= vis[nt][e])) x = -INFINITY;
-                            top[nt][e] = fmaxf(top[nt][e], x);
-                        }
+                        for (int e = 0; e < 2; ++e)
+                            top[nt][e] = fmaxf(top[nt][e], s[half][nt][2 * r + e]);
                     if constexpr (kScores) {
-                        float *to = a.logits + ((first + at + k) * kUnitRows +
-                                                half * kBlockRows + row) * a.log_rows;
+                        float *to = a.logits + ((first + at + k) * kUnitRows + half * kBlockRows +
+                                                row_of(g) + 8 * r) * a.log_rows;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             if (nt * 8 + 2 * t < a.log_rows)
@@ -701,45 +746,55 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
             // Weights, transposed into the second product's operand.
             const float wscale = power_of_two(kWeightExp - exponent_of(vref));
             uint32_t wf[2][NT][kWP][2];
+            auto weigh = [&](auto tag) {
+                constexpr bool kMask = decltype(tag)::value;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float m0 = kMask && m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-                const float m1 = kMask && m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float m0 = kMask && m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+                    const float m1 = kMask && m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                    for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float sc = vs[half][r] * wscale;
-                        float x[2];
+                        for (int r = 0; r < 2; ++r) {
+                            const float sc = vs[half][r] * wscale;
+                            float x[2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float logit = s[half][nt][2 * r + e];
-                            const float p = exp2_approx(logit - (e ? m1 : m0));
-                            l[nt][e] += p;
-                            if constexpr (kMask) {
+                            for (int e = 0; e < 2; ++e) {
+                                const float logit = s[half][nt][2 * r + e];
+                                const float p = exp2_approx(logit - (e ? m1 : m0));
+                                l[nt][e] += p;
                                 // A row that a query does not see adds nothing, whatever
                                 // its parameters are (NaN too).
-                                const bool seen = logit != -INFINITY;
+                                const bool seen = !kMask || logit != -INFINITY;
                                 z[nt][e] = seen ? fmaf(p, vm[half][r], z[nt][e]) : z[nt][e];
                                 x[e] = seen ? p * sc : 0.f;
-                            } else {
-                                z[nt][e] = fmaf(p, vm[half][r], z[nt][e]);
-                                x[e] = p * sc;
                             }
-                        }
 #pragma unroll
-                        for (int part = 0; part < kWP; ++part) {
-                            const __half2 h = __floats2half2_rn(x[0], x[1]);
-                            wf[half][nt][part][r] =
-                                transpose8x8(*reinterpret_cast<const uint32_t *>(&h));
-                            if constexpr (kWP > 1) {
-                                const float2 back = __half22float2(h);
-                                x[0] -= back.x;
-                                x[1] -= back.y;
+                            for (int part = 0; part < kWP; ++part) {
+                                const __half2 h = __floats2half2_rn(x[0], x[1]);
+                                wf[half][nt][part][r] = *reinterpret_cast<const uint32_t *>(&h);
+                                if constexpr (kWP > 1) {
+                                    const float2 back = __half22float2(h);
+                                    x[0] -= back.x;
+                                    x[1] -= back.y;
+                                }
                             }
                         }
-                    }
-            }
+                }
+            };
+            if (masked)
+                weigh(std::true_type{});
+            else
+                weigh(std::false_type{});
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int part = 0; part < kWP; ++part)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            wf[half][nt][part][r] = transpose8x8(wf[half][nt][part][r]);
 
             // O^T += V^T W^T: operand rows g and g + 8 of m-tile 4 * v + p are
             // elements p and p + 4 of the lane's word v.
@@ -798,10 +853,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
         for (int k = skip; k < seg_units; k += kWarps) {
             cp_async_wait<kS - 1>();
             __syncwarp();
-            if ((w.unit + k + 1) * kUnitRows > all_see || (bad >> (2 * stage) & 3u))
-                consume(std::true_type{}, k);
-            else
-                consume(std::false_type{}, k);
+            if ((w.unit + k) * kUnitRows < seq.n) consume(k);
             __syncwarp();
             issue(stage);
             stage = stage + 1 == kS ? 0 : stage + 1;
@@ -888,8 +940,8 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
         if (tid == 0 && w.unit == 0 && !whole) {
             // The item goes on in the blocks behind this one.
             RunRecord &rec = a.runs[blockIdx.x];
-            const int64_t all = rec.all, last_unit = first + at + w.units - 1;
-            const int64_t blocks = all < gridDim.x ? all : gridDim.x;
+            const int64_t all = rec.all, blocks = all < gridDim.x ? all : gridDim.x;
+            const int64_t last_unit = first + at + w.units - kItemUnits - 1;
             rec.join_b = w.b;
             rec.join_item = w.item;
             rec.join_slot = slot;
@@ -1015,7 +1067,8 @@ __global__ void __launch_bounds__(kScoreThreads) qkn_kv4_scores_kernel(const Att
     int k = 0, batch = 0;
     while (k < rec.total) {
         const int left = min(w.units - w.unit, rec.total - k);
-        const int batches = (left + kBatch - 1) / kBatch;
+        const int live = min(w.units - kItemUnits - w.unit, left);
+        const int batches = (live + kBatch - 1) / kBatch;
         // Only a head's first tile stands for its units.
         if (w.item < a.pool.Hk) {
             const Seq seq = load_seq<kR>(a, w.b);
@@ -1034,7 +1087,7 @@ __global__ void __launch_bounds__(kScoreThreads) qkn_kv4_scores_kernel(const Att
                 for (int v = 0; v < kBatch; ++v) {
                     const int j = (w.unit + u + v) * kUnitRows + lane;
                     at[v] = -1;
-                    if (u + v < left && j < seq.n) {
+                    if (u + v < live && j < seq.n) {
                         const int64_t page = table[j >> a.pool.log2_page];
                         if (page_ok(a.pool, page))
                             at[v] = ((page * a.pool.Hk + hk) << a.pool.log2_page) +

@@ -204,9 +204,9 @@ AttentionPlan attention_plan(int64_t B, int dtype, int Hq, int Hk, int D, int ma
     p.nt = query_tiles(dtype, D, rows);
     const int64_t kr = 8 * p.nt;
     const int64_t tiles = (rows + kr - 1) / kr;
-    p.max_units = max_kv > 0 ? (max_kv + kUnitRows - 1) / kUnitRows : 1;
+    p.max_units = (max_kv + kUnitRows - 1) / kUnitRows + kItemUnits;
     p.max_items = (int)(tiles * Hk);
-    p.direct = !scores && p.max_units <= kDirectUnits && B * tiles * Hk <= INT32_MAX;
+    p.direct = !scores && p.max_units - kItemUnits <= kDirectUnits && B * tiles * Hk <= INT32_MAX;
     p.log_rows = (int)(rows < kr ? (rows + 1) / 2 * 2 : kr);
     // Sizes may pass 63 bits for arguments that no buffer could have.
     __int128 at = 0;
