@@ -3,9 +3,13 @@
 // Part of libqknorm.so; included by kv4.cu.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "cache.cuh"
 
 namespace {
+
+namespace cg = cooperative_groups;
 
 struct EvictArgs {
     Pool pool;
@@ -35,7 +39,9 @@ __device__ __forceinline__ uint32_t score_key(float s)
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-constexpr int kSelectThreads = 512;
+constexpr int kEvictThreads = 512;
+// Rows that always stay: above every score's key.
+constexpr uint32_t kNewestKey = 0xffffffffu;
 
 __device__ __forceinline__ uint32_t row_key(const EvictArgs &a, const int32_t *table, int hk, int j)
 {
@@ -45,9 +51,266 @@ __device__ __forceinline__ uint32_t row_key(const EvictArgs &a, const int32_t *t
     return score_key(a.scores[((page * a.pool.Hk + hk) << a.pool.log2_page) + off]);
 }
 
-// Exclusive sum of `flag` over the block, and its total.
+// The copy of kept rows [r0, r1) of one head to rows first + ...: a warp to a
+// block of 16 rows where they go, so that the parameters and scores are
+// written as whole lines; D/32 lanes to a row of codes, 16 bytes each.
+// source(r) is the row that becomes row r.
+template <int D, typename Source>
+__device__ __forceinline__ void move_rows(const EvictArgs &a, int64_t b, int hk, int r0, int r1,
+                                          int warp, int warps, Source source)
+{
+    constexpr int kLanes = D / 16;          // 16-byte pieces of a row's K and V codes
+    constexpr int kRows = 32 / kLanes;      // rows of codes a warp copies at once
+    constexpr int kTimes = kBlockRows / kRows;
+    const int lane = threadIdx.x % 32;
+    const int mask = (1 << a.pool.log2_page) - 1;
+    const int32_t *table = a.page_table + b * a.table_stride;
+    const int32_t *to_table = a.dst_table + b * a.dst_stride;
+    for (int blk = r0 / kBlockRows + warp; blk * kBlockRows < r1; blk += warps) {
+        const int row0 = blk * kBlockRows;
+        const int64_t to = to_table[row0 >> a.pool.log2_page];
+        // Lane l looks row l % 16 up; its place in the pool, or -1.
+        const int mine = row0 + lane % kBlockRows;
+        int64_t from = -1, score_from = -1;  // the block of 16 rows, and the score
+        int row = 0;
+        bool bad = false;
+        if (mine >= r0 && mine < r1) {
+            const int src = source(mine);
+            const int64_t page = table[src >> a.pool.log2_page];
+            if (page_ok(a.pool, page) && page_ok(a.pool, to)) {
+                const int off = src & mask;
+                from = page * a.pool.page_bytes + (int64_t)hk * a.pool.head_bytes +
+                       off / kBlockRows * kBlockBytes<D>;
+                row = off % kBlockRows;
+                score_from = ((page * a.pool.Hk + hk) << a.pool.log2_page) + off;
+            } else {
+                bad = true;
+            }
+        }
+        if (__any_sync(0xffffffffu, bad)) {
+            if (bad && lane < kBlockRows) atomicAdd(&g_kv4_bad_pages, 1u);
+            if (!page_ok(a.pool, to)) continue;
+        }
+        uint8_t *db = a.pool.base + to * a.pool.page_bytes + (int64_t)hk * a.pool.head_bytes +
+                      (row0 & mask) / kBlockRows * kBlockBytes<D>;
+        // Codes: lane l has piece l % kLanes (K's pieces, then V's) of rows l / kLanes + ...
+        const int piece = lane % kLanes;
+        const int kv = piece / (kLanes / 2), at = piece % (kLanes / 2) * 16;
+        uint4 codes[kTimes];
+        bool there[kTimes];
+#pragma unroll
+        for (int i = 0; i < kTimes; ++i) {
+            const int r = i * kRows + lane / kLanes;
+            const int64_t place = __shfl_sync(0xffffffffu, from, r);
+            const int place_row = __shfl_sync(0xffffffffu, row, r);
+            there[i] = place >= 0;
+            if (there[i])
+                codes[i] = *reinterpret_cast<const uint4 *>(a.pool.base + place + kv * 8 * D +
+                                                            place_row * (D / 2) + at);
+        }
+        uint32_t par = 0;
+        float score = 0.f;
+        if (from >= 0) {
+            par = *reinterpret_cast<const uint32_t *>(a.pool.base + from + 16 * D +
+                                                      lane / kBlockRows * 64 + row * 4);
+            if (lane < kBlockRows) score = a.scores[score_from];
+        }
+#pragma unroll
+        for (int i = 0; i < kTimes; ++i)
+            if (there[i])
+                *reinterpret_cast<uint4 *>(db + kv * 8 * D +
+                                           (i * kRows + lane / kLanes) * (D / 2) + at) = codes[i];
+        if (from >= 0) {
+            *reinterpret_cast<uint32_t *>(db + 16 * D + lane * 4) = par;
+            if (lane < kBlockRows)
+                a.scores[((to * a.pool.Hk + hk) << a.pool.log2_page) + (mine & mask)] = score;
+        }
+    }
+}
+
+// One cluster per (sequence, head).  Its blocks hold equal runs of the rows'
+// keys in shared memory.  The border (the budget-th largest key) is found two
+// bits at a time by counting the keys at or above three candidates, which
+// takes the same time for every distribution of scores; then each block knows
+// how many of its rows stay and how many stay before them, lists its rows in
+// place of their keys, and copies them.
+template <int D>
+__global__ void __launch_bounds__(kEvictThreads) qkn_kv4_evict_kernel(const EvictArgs a)
+{
+    constexpr int kWarpsOf = kEvictThreads / 32;
+    extern __shared__ __align__(16) uint32_t keys[];
+    __shared__ int counts[16][4];  // of each step, summed over the cluster in block 0
+    __shared__ int warp_gt[kWarpsOf], warp_eq[kWarpsOf];
+    __shared__ int block_gt, block_eq;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    if (tid < 64) counts[tid / 4][tid % 4] = 0;
+    pdl_wait_then_release();
+
+    const int64_t item = blockIdx.x / blocks;
+    const int64_t b = item / a.pool.Hk;
+    const int hk = (int)(item - b * a.pool.Hk);
+    const int n = evict_len(a, b);
+    const int32_t *table = a.page_table + b * a.table_stride;
+    int32_t *kept = a.kept + item * a.budget;
+    const int keep = n < a.budget ? n : a.budget;
+    if (hk == 0 && rank == 0 && tid == 0) a.new_lens[b] = keep;
+    for (int j = keep + rank * kEvictThreads + tid; j < a.budget; j += blocks * kEvictThreads)
+        kept[j] = -1;
+    if (n <= a.budget) {  // all stay; the same for every block of the cluster
+        const int per = ((n + blocks - 1) / blocks + 15) / 16 * 16;
+        const int r0 = min(n, rank * per), r1 = min(n, r0 + per);
+        for (int j = r0 + tid; j < r1; j += kEvictThreads) kept[j] = j;
+        move_rows<D>(a, b, hk, r0, r1, warp, kWarpsOf, [](int r) { return r; });
+        return;
+    }
+
+    // This block's rows, four to a load; a thread's share is `each` in a row.
+    const int each = ((n + blocks * kEvictThreads - 1) / (blocks * kEvictThreads) + 3) / 4 * 4;
+    const int r0 = min(n, rank * each * kEvictThreads);
+    const int old = n - a.recent;
+#pragma unroll 4
+    for (int i = tid * 4; i < each * kEvictThreads; i += kEvictThreads * 4) {
+        const int j = r0 + i;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool ok = false;
+        if (j < n) {
+            const int64_t page = table[j >> a.pool.log2_page];
+            ok = page_ok(a.pool, page);
+            if (ok)
+                s = *reinterpret_cast<const float4 *>(
+                    a.scores + ((page * a.pool.Hk + hk) << a.pool.log2_page) +
+                    (j & ((1 << a.pool.log2_page) - 1)));
+        }
+        const float f[4] = {s.x, s.y, s.z, s.w};
+        uint32_t k[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            k[e] = j + e >= n ? 0u : (j + e >= old ? kNewestKey : (ok ? score_key(f[e]) : 0u));
+        *reinterpret_cast<uint4 *>(keys + i) = make_uint4(k[0], k[1], k[2], k[3]);
+    }
+    if (blocks > 1)
+        cluster.sync();
+    else
+        __syncthreads();
+
+    // Rows behind the last have key 0 too, but sit behind every row of key 0,
+    // and there are budget rows before them.
+    const uint32_t *mine = keys + tid * each;
+    uint32_t border = 0;
+    int above = 0;  // keys above the border's candidates so far
+    for (int step = 0; step < 16; ++step) {
+        const int shift = 30 - 2 * step;
+        const uint32_t c1 = border + (1u << shift), c2 = border + (2u << shift),
+                       c3 = border + (3u << shift);
+        int n1 = 0, n2 = 0, n3 = 0;
+        for (int i = 0; i < each; i += 4) {
+            const uint4 k = *reinterpret_cast<const uint4 *>(mine + i);
+            n1 += (k.x >= c1) + (k.y >= c1) + (k.z >= c1) + (k.w >= c1);
+            n2 += (k.x >= c2) + (k.y >= c2) + (k.z >= c2) + (k.w >= c2);
+            n3 += (k.x >= c3) + (k.y >= c3) + (k.z >= c3) + (k.w >= c3);
+        }
+        n1 = __reduce_add_sync(0xffffffffu, n1);
+        n2 = __reduce_add_sync(0xffffffffu, n2);
+        n3 = __reduce_add_sync(0xffffffffu, n3);
+        int *sum = blocks > 1 ? cluster.map_shared_rank(&counts[step][0], 0) : &counts[step][0];
+        if (lane < 3) atomicAdd(sum + lane, lane == 0 ? n1 : (lane == 1 ? n2 : n3));
+        if (blocks > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+        n1 = sum[0];
+        n2 = sum[1];
+        n3 = sum[2];
+        if (n3 >= a.budget)
+            border = c3;
+        else if (n2 >= a.budget) {
+            border = c2;
+            above = n3;
+        } else if (n1 >= a.budget) {
+            border = c1;
+            above = n2;
+        } else
+            above = n1;
+    }
+    const int ties = a.budget - above;  // of the rows on the border, the first ones stay
+
+    // Ranks: rows above and on the border, by thread, warp, block.
+    int gt = 0, eq = 0;
+    for (int i = 0; i < each; i += 4) {
+        const uint4 k = *reinterpret_cast<const uint4 *>(mine + i);
+        gt += (k.x > border) + (k.y > border) + (k.z > border) + (k.w > border);
+        eq += (k.x == border) + (k.y == border) + (k.z == border) + (k.w == border);
+    }
+    int gt_sum = gt, eq_sum = eq;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, gt_sum, o);
+        const int y = __shfl_up_sync(0xffffffffu, eq_sum, o);
+        if (lane >= o) {
+            gt_sum += x;
+            eq_sum += y;
+        }
+    }
+    if (lane == 31) {
+        warp_gt[warp] = gt_sum;
+        warp_eq[warp] = eq_sum;
+    }
+    __syncthreads();
+    int gt_before = gt_sum - gt, eq_before = eq_sum - eq, gt_all = 0, eq_all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarpsOf; ++w) {
+        if (w < warp) {
+            gt_before += warp_gt[w];
+            eq_before += warp_eq[w];
+        }
+        gt_all += warp_gt[w];
+        eq_all += warp_eq[w];
+    }
+    int gt_blocks = 0, eq_blocks = 0;  // in the blocks before this one
+    if (blocks > 1) {
+        if (tid == 0) {
+            block_gt = gt_all;
+            block_eq = eq_all;
+        }
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {
+            gt_blocks += *cluster.map_shared_rank(&block_gt, r);
+            eq_blocks += *cluster.map_shared_rank(&block_eq, r);
+        }
+        cluster.sync();  // no block leaves while another reads its counts
+    }
+    // The block's kept rows are [first, first + kept_here) of the head's.
+    const int first = gt_blocks + min(eq_blocks, ties);
+    const int last = gt_blocks + gt_all + min(eq_blocks + eq_all, ties);
+    // Which of the thread's rows stay (`each` is at most 96), then their list
+    // in place of the keys.
+    uint32_t stay[3] = {};
+    int e = eq_blocks + eq_before;
+    for (int i = 0; i < each; ++i) {
+        const uint32_t k = mine[i];
+        const bool on = k == border;
+        if (k > border || (on && e < ties)) stay[i / 32] |= 1u << (i % 32);
+        e += on;
+    }
+    int at = gt_blocks + gt_before + min(eq_blocks + eq_before, ties) - first;
+    __syncthreads();
+#pragma unroll
+    for (int word = 0; word < 3; ++word)
+        for (uint32_t m = stay[word]; m != 0; m &= m - 1)
+            keys[at++] = (uint32_t)(r0 + tid * each + word * 32 + __ffs(m) - 1);
+    __syncthreads();
+    for (int i = tid; i < last - first; i += kEvictThreads) kept[first + i] = (int32_t)keys[i];
+    move_rows<D>(a, b, hk, first, last, warp, kWarpsOf,
+                 [&](int r) { return (int)keys[r - first]; });
+}
+
+// Sequences too long for a cluster's shared memory: the same choice by one
+// block over the scores in memory, and a copy of its own.
 __device__ __forceinline__ int block_rank(bool flag, int *sums, int &total)
 {
+    // Exclusive sum of `flag` over the block, and its total.
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const uint32_t m = __ballot_sync(0xffffffffu, flag);
     __syncthreads();
@@ -55,19 +318,17 @@ __device__ __forceinline__ int block_rank(bool flag, int *sums, int &total)
     __syncthreads();
     int before = 0;
     total = 0;
-    for (int w = 0; w < kSelectThreads / 32; ++w) {
+    for (int w = 0; w < kEvictThreads / 32; ++w) {
         if (w == warp) before = total;
         total += sums[w];
     }
     return before + __popc(m & ((1u << lane) - 1));
 }
 
-// One block per (sequence, head): the k-th largest key by four passes over
-// its 8-bit digits, then the kept rows' numbers in order.
-__global__ void __launch_bounds__(kSelectThreads) qkn_kv4_select_kernel(EvictArgs a)
+__global__ void __launch_bounds__(kEvictThreads) qkn_kv4_select_kernel(const EvictArgs a)
 {
     __shared__ int hist[256];
-    __shared__ int sums[kSelectThreads / 32];
+    __shared__ int sums[kEvictThreads / 32];
     __shared__ int s_digit, s_left;
     pdl_wait_then_release();
     const int64_t b = blockIdx.x / a.pool.Hk;
@@ -78,45 +339,40 @@ __global__ void __launch_bounds__(kSelectThreads) qkn_kv4_select_kernel(EvictArg
     const int keep = n < a.budget ? n : a.budget;
     if (hk == 0 && threadIdx.x == 0) a.new_lens[b] = keep;
     if (n <= a.budget) {
-        for (int j = threadIdx.x; j < a.budget; j += kSelectThreads) kept[j] = j < n ? j : -1;
+        for (int j = threadIdx.x; j < a.budget; j += kEvictThreads) kept[j] = j < n ? j : -1;
         return;
     }
-    const int old = n - a.recent;            // rows that compete
-    int left = a.budget - a.recent;          // how many of them stay
+    const int old = n - a.recent;
+    int left = a.budget;
     uint32_t prefix = 0, mask = 0;
-    if (left > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = threadIdx.x; i < 256; i += kSelectThreads) hist[i] = 0;
-            __syncthreads();
-            for (int j = threadIdx.x; j < old; j += kSelectThreads) {
-                const uint32_t key = row_key(a, table, hk, j);
-                if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
-            }
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                int d = 255, above = 0;
-                while (d > 0 && above + hist[d] < left) above += hist[d--];
-                s_digit = d;
-                s_left = left - above;
-            }
-            __syncthreads();
-            prefix |= (uint32_t)s_digit << shift;
-            mask |= 255u << shift;
-            left = s_left;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        for (int i = threadIdx.x; i < 256; i += kEvictThreads) hist[i] = 0;
+        __syncthreads();
+        for (int j = threadIdx.x; j < n; j += kEvictThreads) {
+            const uint32_t key = j < old ? row_key(a, table, hk, j) : kNewestKey;
+            if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
         }
-    } else {
-        prefix = 0xffffffffu;
-        left = 0;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            int d = 255, above = 0;
+            while (d > 0 && above + hist[d] < left) above += hist[d--];
+            s_digit = d;
+            s_left = left - above;
+        }
+        __syncthreads();
+        prefix |= (uint32_t)s_digit << shift;
+        mask |= 255u << shift;
+        left = s_left;
     }
     // Rows above the border key stay, and the first `left` of those on it.
     int out = 0, ties = 0;
-    for (int base = 0; base < n; base += kSelectThreads) {
+    for (int base = 0; base < n; base += kEvictThreads) {
         const int j = base + threadIdx.x;
-        const uint32_t key = j < old ? row_key(a, table, hk, j) : 0u;
-        const bool tie = j < old && key == prefix;
+        const uint32_t key = j < old ? row_key(a, table, hk, j) : kNewestKey;
+        const bool tie = j < n && key == prefix;
         int total;
         const int rank = block_rank(tie, sums, total);
-        const bool stay = j < n && (j >= old || key > prefix || (tie && ties + rank < left));
+        const bool stay = j < n && (key > prefix || (tie && ties + rank < left));
         ties += total;
         const int at = block_rank(stay, sums, total);
         if (stay) kept[out + at] = j;
@@ -124,52 +380,18 @@ __global__ void __launch_bounds__(kSelectThreads) qkn_kv4_select_kernel(EvictArg
     }
 }
 
-// Copies of the kept rows: D/16 lanes to a row, a lane copies 16 bytes of its
-// codes (half the lanes K, half V), and the first three the parameters and
-// the score.
 template <int D>
-__global__ void __launch_bounds__(256) qkn_kv4_move_kernel(EvictArgs a)
+__global__ void __launch_bounds__(kEvictThreads) qkn_kv4_move_kernel(const EvictArgs a)
 {
-    constexpr int kLanes = D / 16;
     pdl_wait_then_release();
-    const int64_t rows = a.B * a.pool.Hk * a.budget;
-    const int lane = threadIdx.x % kLanes;
-    const int mask = (1 << a.pool.log2_page) - 1;
-    for (int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / kLanes; r < rows;
-         r += (int64_t)gridDim.x * blockDim.x / kLanes) {
-        const int src = a.kept[r];
-        if (src < 0) continue;
-        const int64_t item = r / a.budget;
-        const int dst = (int)(r - item * a.budget);
-        const int64_t b = item / a.pool.Hk;
-        const int hk = (int)(item - b * a.pool.Hk);
-        const int64_t from = a.page_table[b * a.table_stride + (src >> a.pool.log2_page)];
-        const int64_t to = a.dst_table[b * a.dst_stride + (dst >> a.pool.log2_page)];
-        if (!page_ok(a.pool, from) || !page_ok(a.pool, to)) {
-            if (lane == 0) atomicAdd(&g_kv4_bad_pages, 1u);
-            continue;
-        }
-        const int so = src & mask, to_off = dst & mask;
-        const uint8_t *sb = a.pool.base + from * a.pool.page_bytes +
-                            (int64_t)hk * a.pool.head_bytes + so / kBlockRows * kBlockBytes<D>;
-        uint8_t *db = a.pool.base + to * a.pool.page_bytes + (int64_t)hk * a.pool.head_bytes +
-                      to_off / kBlockRows * kBlockBytes<D>;
-        const int sr = so % kBlockRows, dr = to_off % kBlockRows;
-        const int kv = lane / (kLanes / 2), part = lane % (kLanes / 2);
-        const int at = kv * 8 * D + part * 16;
-        const uint4 codes = *reinterpret_cast<const uint4 *>(sb + at + sr * (D / 2));
-        uint32_t word = 0;
-        if (lane < 2)
-            word = *reinterpret_cast<const uint32_t *>(sb + 16 * D + lane * 64 + sr * 4);
-        else if (lane == 2)
-            word = __float_as_uint(
-                a.scores[((from * a.pool.Hk + hk) << a.pool.log2_page) + so]);
-        *reinterpret_cast<uint4 *>(db + at + dr * (D / 2)) = codes;
-        if (lane < 2)
-            *reinterpret_cast<uint32_t *>(db + 16 * D + lane * 64 + dr * 4) = word;
-        else if (lane == 2)
-            a.scores[((to * a.pool.Hk + hk) << a.pool.log2_page) + to_off] = __uint_as_float(word);
-    }
+    const int64_t item = blockIdx.x;
+    const int64_t b = item / a.pool.Hk;
+    const int n = evict_len(a, b), keep = n < a.budget ? n : a.budget;
+    const int32_t *kept = a.kept + item * a.budget;
+    const int warps = gridDim.y * (kEvictThreads / 32);
+    move_rows<D>(a, b, (int)(item - b * a.pool.Hk), 0, keep,
+                 blockIdx.y * (kEvictThreads / 32) + threadIdx.x / 32, warps,
+                 [&](int r) { return kept[r]; });
 }
 
 }  // namespace

@@ -290,6 +290,64 @@ struct Attention {
     }
 };
 
+// ---------------------------------------------------------------- eviction --
+// Rows of a head that a cluster holds at most: 96 to a thread, 8 blocks.
+constexpr int kEvictEach = 96;
+constexpr int kMaxCluster = 8;
+
+template <int D>
+int run_evict(const EvictArgs &a, cudaStream_t stream)
+{
+    static std::atomic<int> cache[kMaxDevices];
+    auto kern = qkn_kv4_evict_kernel<D>;
+    constexpr int max_smem = kEvictEach * kEvictThreads * 4;
+    const int64_t items = a.B * a.pool.Hk;
+    const int64_t rows = a.max_pages << a.pool.log2_page;
+    int dev = 0, sms = 0, rc;
+    if ((rc = device_sms(&sms)) != QKN_OK) return rc;
+    if (rows > (int64_t)kEvictEach * kEvictThreads * kMaxCluster) {
+        rc = launch(qkn_kv4_select_kernel, dim3((unsigned)items), kEvictThreads, 0, stream, a);
+        if (rc != QKN_OK) return rc;
+        int64_t each = (4 * (int64_t)sms + items - 1) / items;
+        if (each > a.budget / 256 + 1) each = a.budget / 256 + 1;
+        return launch(qkn_kv4_move_kernel<D>, dim3((unsigned)items, (unsigned)each), kEvictThreads,
+                      0, stream, a);
+    }
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (cache[dev].load(std::memory_order_acquire) == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+        if (e != cudaSuccess) return cuda_fail(e);
+        cache[dev].store(1, std::memory_order_release);
+    }
+    // Blocks to a head: what its rows need, and more while heads are few and
+    // each block keeps kEvictThreads * 8 rows or more.
+    int cluster = 1;
+    while (cluster < kMaxCluster &&
+           (rows > (int64_t)cluster * kEvictThreads * kEvictEach ||
+            (rows > (int64_t)cluster * kEvictThreads * 8 && items * cluster * 2 <= 2 * sms)))
+        cluster *= 2;
+    const int64_t each =
+        ((rows + cluster * kEvictThreads - 1) / (cluster * kEvictThreads) + 3) / 4 * 4;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * cluster));
+    cfg.blockDim = dim3(kEvictThreads);
+    cfg.dynamicSmemBytes = (size_t)each * kEvictThreads * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? QKN_OK : cuda_fail(e);
+}
+
 int attention_shape(int64_t B, int dtype, int Hq, int Hk, int D, int max_q, int64_t max_kv)
 {
     if (elem_size(dtype) == 0) return QKN_ERR_UNSUPPORTED;
@@ -425,7 +483,7 @@ int qknorm_kv4_evict(void *pool, int64_t num_pages, int page_size, int Hk, int D
         return QKN_ERR_SHAPE;
     if (B < 0 || table_stride < max_pages || dst_stride < dst_pages || budget < 1 ||
         budget > dst_pages * page_size || recent < 0 || recent > budget || Hk < 1 ||
-        B > INT32_MAX / Hk)
+        B > INT32_MAX / Hk / kMaxCluster)
         return QKN_ERR_SHAPE;
     if (B == 0) return QKN_OK;
     int rc = check_pool(pool, num_pages, page_size, Hk, D, &p);
@@ -433,7 +491,7 @@ int qknorm_kv4_evict(void *pool, int64_t num_pages, int page_size, int Hk, int D
     if (scores == nullptr || (max_pages > 0 && page_table == nullptr) || kv_lens == nullptr ||
         dst_table == nullptr || new_lens == nullptr || kept == nullptr)
         return QKN_ERR_NULL;
-    if (!aligned(scores, 4) || !aligned(page_table, 4) || !aligned(kv_lens, 4) ||
+    if (!aligned(scores, 16) || !aligned(page_table, 4) || !aligned(kv_lens, 4) ||
         !aligned(dst_table, 4) || !aligned(new_lens, 4) || !aligned(kept, 4))
         return QKN_ERR_ALIGN;
     EvictArgs a = {};
@@ -451,13 +509,11 @@ int qknorm_kv4_evict(void *pool, int64_t num_pages, int page_size, int Hk, int D
     a.new_lens = new_lens;
     a.kept = kept;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    rc = launch(qkn_kv4_select_kernel, dim3((unsigned)(B * Hk)), kSelectThreads, 0, s, a);
-    if (rc != QKN_OK) return rc;
-    unsigned grid = 0;
-    if ((rc = stream_grid((uint64_t)B * Hk * budget, D / 16, 8, &grid)) != QKN_OK) return rc;
-    auto kern = D == 64 ? qkn_kv4_move_kernel<64>
-                        : (D == 128 ? qkn_kv4_move_kernel<128> : qkn_kv4_move_kernel<256>);
-    return launch(kern, dim3(grid), 256, 0, s, a);
+    switch (D) {
+    case 64: return run_evict<64>(a, s);
+    case 128: return run_evict<128>(a, s);
+    default: return run_evict<256>(a, s);
+    }
 }
 
 int qknorm_kv4_bad_pages(unsigned int *count)

@@ -333,7 +333,8 @@ def test_offsets_beyond_32_bits():
     (1, 64, 16, 1, 0), (2, 128, 64, 100, 30), (3, 256, 32, 64, 64), (8, 128, 128, 257, 0),
     (2, 64, 256, 300, 299)])
 @pytest.mark.parametrize("kind", ["spread", "ties", "special"])
-def test_evict(Hk, D, page, budget, recent, kind):
+@pytest.mark.parametrize("wide", [False, True])
+def test_evict(Hk, D, page, budget, recent, kind, wide):
     lens = [0, 1, budget - 1, budget, budget + 1, 700, 1500]
     cache, _, table, _ = problem(budget, lens, [1] * len(lens), 1, Hk, D, page, "bf16", True)
     g = gen(budget + 1)
@@ -354,6 +355,8 @@ def test_evict(Hk, D, page, budget, recent, kind):
     to = old + torch.randperm(B * dp, generator=g, device="cuda").to(torch.int32).view(B, dp)
     before = ku.Held(both)
     sb = both.scores.cpu().numpy()
+    if wide:  # a table for sequences that no cluster holds
+        table = torch.cat([table, torch.full((B, 400000 // page), -1, dtype=torch.int32)], 1)
     new_lens, kept = qkn.qknorm_kv4_evict(both, table.cuda(),
                                           torch.tensor(lens, dtype=torch.int32, device="cuda"),
                                           to, budget, recent)
@@ -378,8 +381,9 @@ def test_evict(Hk, D, page, budget, recent, kind):
             assert np.all(after.codes[0][to[b][rest // page], h, rest % page, 0] == 0xA)
 
 
-@pytest.mark.parametrize("n,budget", [(40000, 5000), (131072, 16384), (20000, 19999)])
-def test_evict_long(n, budget):
+@pytest.mark.parametrize("n,budget,wide", [(40000, 5000, 0), (131072, 16384, 0), (20000, 19999, 0),
+                                           (300001, 70000, 0), (30011, 300, 4000)])
+def test_evict_long(n, budget, wide):
     page = 128
     cache, _, table, _ = problem(3, [n, 777], [1, 1], 1, 2, 64, page, "bf16", True)
     g = gen(4)
@@ -390,6 +394,7 @@ def test_evict_long(n, budget):
                         2, 64, page, torch.cat([s, s.new_zeros((2 * dp,) + s.shape[1:])]))
     to = torch.arange(cache.num_pages, cache.num_pages + 2 * dp, dtype=torch.int32,
                       device="cuda").view(2, dp)
+    table = torch.cat([table, torch.full((2, wide), -1, dtype=torch.int32)], 1)
     lens, kept = qkn.qknorm_kv4_evict(both, table.cuda(),
                                       torch.tensor([n, 777], dtype=torch.int32, device="cuda"),
                                       to, budget, budget // 8)
