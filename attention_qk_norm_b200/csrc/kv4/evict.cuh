@@ -129,23 +129,32 @@ __device__ __forceinline__ void move_rows(const EvictArgs &a, int64_t b, int hk,
 }
 
 // One cluster per (sequence, head).  Its blocks hold equal runs of the rows'
-// keys in shared memory.  The border (the budget-th largest key) is found two
-// bits at a time by counting the keys at or above three candidates, which
-// takes the same time for every distribution of scores; then each block knows
-// how many of its rows stay and how many stay before them, lists its rows in
-// place of their keys, and copies them.
+// keys in shared memory.  The border (the budget-th largest key) is found in
+// three digits of 11, 11 and 10 bits: each block counts its keys by digit, and
+// each adds the blocks' counts up for itself.  (Counting the keys at or above
+// three candidates, two bits at a time, took sixteen such rounds and measured
+// 110 us where this takes less, see kEvictThreads' table in the tests' sizes.)
+// Then each block knows how many of its rows stay and how many stay before
+// them, lists its rows in place of their keys, and copies them.
+constexpr int kBins = 2048;
+constexpr int kEvictStatic = 3 * kBins * 4 + 1024;  // shared memory beside the keys
+
+// Words from one thread's keys to the next's: `each`, made an odd number of
+// 16-byte steps so that eight lanes' loads fall on different banks.
+__host__ __device__ __forceinline__ int key_stride(int each) { return each % 8 == 0 ? each + 4 : each; }
+
 template <int D>
 __global__ void __launch_bounds__(kEvictThreads) qkn_kv4_evict_kernel(const EvictArgs a)
 {
     constexpr int kWarpsOf = kEvictThreads / 32;
     extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ int counts[16][4];  // of each step, summed over the cluster in block 0
+    __shared__ __align__(16) int hist[3][kBins];
     __shared__ int warp_gt[kWarpsOf], warp_eq[kWarpsOf];
-    __shared__ int block_gt, block_eq;
+    __shared__ int block_gt, block_eq, s_digit, s_left;
     cg::cluster_group cluster = cg::this_cluster();
     const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    if (tid < 64) counts[tid / 4][tid % 4] = 0;
+    for (int i = tid; i < 3 * kBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
     pdl_wait_then_release();
 
     const int64_t item = blockIdx.x / blocks;
@@ -168,6 +177,7 @@ __global__ void __launch_bounds__(kEvictThreads) qkn_kv4_evict_kernel(const Evic
 
     // This block's rows, four to a load; a thread's share is `each` in a row.
     const int each = ((n + blocks * kEvictThreads - 1) / (blocks * kEvictThreads) + 3) / 4 * 4;
+    const int stride = key_stride(each);
     const int r0 = min(n, rank * each * kEvictThreads);
     const int old = n - a.recent;
 #pragma unroll 4
@@ -188,53 +198,77 @@ __global__ void __launch_bounds__(kEvictThreads) qkn_kv4_evict_kernel(const Evic
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             k[e] = j + e >= n ? 0u : (j + e >= old ? kNewestKey : (ok ? score_key(f[e]) : 0u));
-        *reinterpret_cast<uint4 *>(keys + i) = make_uint4(k[0], k[1], k[2], k[3]);
+        const int owner = i / each;
+        *reinterpret_cast<uint4 *>(keys + owner * stride + (i - owner * each)) =
+            make_uint4(k[0], k[1], k[2], k[3]);
     }
-    if (blocks > 1)
-        cluster.sync();
-    else
-        __syncthreads();
+    __syncthreads();
 
     // Rows behind the last have key 0 too, but sit behind every row of key 0,
     // and there are budget rows before them.
-    const uint32_t *mine = keys + tid * each;
+    const uint32_t *mine = keys + tid * stride;
     uint32_t border = 0;
-    int above = 0;  // keys above the border's candidates so far
-    for (int step = 0; step < 16; ++step) {
-        const int shift = 30 - 2 * step;
-        const uint32_t c1 = border + (1u << shift), c2 = border + (2u << shift),
-                       c3 = border + (3u << shift);
-        int n1 = 0, n2 = 0, n3 = 0;
+    int left = a.budget;  // how many of the keys that share the border's digits so far stay
+#pragma unroll
+    for (int digit = 0; digit < 3; ++digit) {
+        const int shift = digit == 0 ? 21 : (digit == 1 ? 10 : 0);
+        const uint32_t bins = digit == 2 ? 1023u : 2047u;
+        const uint32_t mask = digit == 0 ? 0u : (digit == 1 ? 0xffe00000u : 0xfffffc00u);
         for (int i = 0; i < each; i += 4) {
             const uint4 k = *reinterpret_cast<const uint4 *>(mine + i);
-            n1 += (k.x >= c1) + (k.y >= c1) + (k.z >= c1) + (k.w >= c1);
-            n2 += (k.x >= c2) + (k.y >= c2) + (k.z >= c2) + (k.w >= c2);
-            n3 += (k.x >= c3) + (k.y >= c3) + (k.z >= c3) + (k.w >= c3);
+            if ((k.x & mask) == border) atomicAdd(&hist[digit][k.x >> shift & bins], 1);
+            if ((k.y & mask) == border) atomicAdd(&hist[digit][k.y >> shift & bins], 1);
+            if ((k.z & mask) == border) atomicAdd(&hist[digit][k.z >> shift & bins], 1);
+            if ((k.w & mask) == border) atomicAdd(&hist[digit][k.w >> shift & bins], 1);
         }
-        n1 = __reduce_add_sync(0xffffffffu, n1);
-        n2 = __reduce_add_sync(0xffffffffu, n2);
-        n3 = __reduce_add_sync(0xffffffffu, n3);
-        int *sum = blocks > 1 ? cluster.map_shared_rank(&counts[step][0], 0) : &counts[step][0];
-        if (lane < 3) atomicAdd(sum + lane, lane == 0 ? n1 : (lane == 1 ? n2 : n3));
         if (blocks > 1)
             cluster.sync();
         else
             __syncthreads();
-        n1 = sum[0];
-        n2 = sum[1];
-        n3 = sum[2];
-        if (n3 >= a.budget)
-            border = c3;
-        else if (n2 >= a.budget) {
-            border = c2;
-            above = n3;
-        } else if (n1 >= a.budget) {
-            border = c1;
-            above = n2;
-        } else
-            above = n1;
+        // Four bins to a thread, the highest first.
+        const int bin = kBins - 4 - 4 * tid;
+        int4 c = *reinterpret_cast<const int4 *>(&hist[digit][bin]);
+        if (blocks > 1) {
+            c = make_int4(0, 0, 0, 0);
+            for (int r = 0; r < blocks; ++r) {
+                const int4 x = *reinterpret_cast<const int4 *>(
+                    cluster.map_shared_rank(&hist[digit][bin], r));
+                c.x += x.x;
+                c.y += x.y;
+                c.z += x.z;
+                c.w += x.w;
+            }
+        }
+        const int own = c.x + c.y + c.z + c.w;
+        int sum = own;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += x;
+        }
+        if (lane == 31) warp_gt[warp] = sum;
+        __syncthreads();
+        int above = sum - own;
+#pragma unroll
+        for (int w = 0; w < kWarpsOf; ++w)
+            if (w < warp) above += warp_gt[w];
+        if (above < left && left <= above + own) {  // the border's digit is one of these four
+            int d = bin + 3;
+            const int four[4] = {c.w, c.z, c.y, c.x};
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (d == bin + 3 - e && above + four[e] < left) {
+                    above += four[e];
+                    --d;
+                }
+            s_digit = d;
+            s_left = left - above;
+        }
+        __syncthreads();
+        border |= (uint32_t)s_digit << shift;
+        left = s_left;
     }
-    const int ties = a.budget - above;  // of the rows on the border, the first ones stay
+    const int ties = left;  // of the rows on the border, the first ones stay
 
     // Ranks: rows above and on the border, by thread, warp, block.
     int gt = 0, eq = 0;

@@ -300,7 +300,7 @@ int run_evict(const EvictArgs &a, cudaStream_t stream)
 {
     static std::atomic<int> cache[kMaxDevices];
     auto kern = qkn_kv4_evict_kernel<D>;
-    constexpr int max_smem = kEvictEach * kEvictThreads * 4;
+    constexpr int max_smem = (kEvictEach + 4) * kEvictThreads * 4;
     const int64_t items = a.B * a.pool.Hk;
     const int64_t rows = a.max_pages << a.pool.log2_page;
     int dev = 0, sms = 0, rc;
@@ -327,12 +327,11 @@ int run_evict(const EvictArgs &a, cudaStream_t stream)
            (rows > (int64_t)cluster * kEvictThreads * kEvictEach ||
             (rows > (int64_t)cluster * kEvictThreads * 8 && items * cluster * 2 <= 2 * sms)))
         cluster *= 2;
-    const int64_t each =
-        ((rows + cluster * kEvictThreads - 1) / (cluster * kEvictThreads) + 3) / 4 * 4;
+    const int each = (int)((rows + cluster * kEvictThreads - 1) / (cluster * kEvictThreads) + 3) / 4 * 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items * cluster));
     cfg.blockDim = dim3(kEvictThreads);
-    cfg.dynamicSmemBytes = (size_t)each * kEvictThreads * 4;
+    cfg.dynamicSmemBytes = (size_t)key_stride(each) * kEvictThreads * 4;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
