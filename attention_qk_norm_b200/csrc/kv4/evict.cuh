@@ -51,10 +51,10 @@ __device__ __forceinline__ uint32_t row_key(const EvictArgs &a, const int32_t *t
     return score_key(a.scores[((page * a.pool.Hk + hk) << a.pool.log2_page) + off]);
 }
 
-// The copy of kept rows [r0, r1) of one head to rows first + ...: a warp to a
-// block of 16 rows where they go, so that the parameters and scores are
-// written as whole lines; D/32 lanes to a row of codes, 16 bytes each.
-// source(r) is the row that becomes row r.
+// The copy of kept rows [r0, r1) of one head, source(r) the row that becomes
+// row r: a warp to a block of 16 rows where they go, so that the parameters
+// and scores are written as whole lines; D/16 lanes to a row's codes, 16 bytes
+// each.  The next block's rows are looked up while this one's are under way.
 template <int D, typename Source>
 __device__ __forceinline__ void move_rows(const EvictArgs &a, int64_t b, int hk, int r0, int r1,
                                           int warp, int warps, Source source)
@@ -66,64 +66,67 @@ __device__ __forceinline__ void move_rows(const EvictArgs &a, int64_t b, int hk,
     const int mask = (1 << a.pool.log2_page) - 1;
     const int32_t *table = a.page_table + b * a.table_stride;
     const int32_t *to_table = a.dst_table + b * a.dst_stride;
-    for (int blk = r0 / kBlockRows + warp; blk * kBlockRows < r1; blk += warps) {
-        const int row0 = blk * kBlockRows;
-        const int64_t to = to_table[row0 >> a.pool.log2_page];
-        // Lane l looks row l % 16 up; its place in the pool, or -1.
-        const int mine = row0 + lane % kBlockRows;
-        int64_t from = -1, score_from = -1;  // the block of 16 rows, and the score
-        int row = 0;
-        bool bad = false;
-        if (mine >= r0 && mine < r1) {
-            const int src = source(mine);
-            const int64_t page = table[src >> a.pool.log2_page];
-            if (page_ok(a.pool, page) && page_ok(a.pool, to)) {
-                const int off = src & mask;
-                from = page * a.pool.page_bytes + (int64_t)hk * a.pool.head_bytes +
-                       off / kBlockRows * kBlockBytes<D>;
-                row = off % kBlockRows;
-                score_from = ((page * a.pool.Hk + hk) << a.pool.log2_page) + off;
-            } else {
-                bad = true;
-            }
+    uint8_t *head = a.pool.base + (int64_t)hk * a.pool.head_bytes;
+    const int piece = lane % kLanes;  // K's pieces of a row, then V's
+    const int code_at = piece / (kLanes / 2) * 8 * D + piece % (kLanes / 2) * 16;
+    // Lane l looks row l % 16 of a block up: its page (-1: none) and place.
+    int page, off, to;
+    const auto look = [&](int blk) {
+        const int r = blk * kBlockRows + lane % kBlockRows;
+        page = to = -1;
+        off = 0;
+        if (blk * kBlockRows >= r1) return;
+        to = to_table[blk * kBlockRows >> a.pool.log2_page];
+        if (r >= r0 && r < r1) {
+            const int src = source(r);
+            page = table[src >> a.pool.log2_page];
+            off = src & mask;
         }
-        if (__any_sync(0xffffffffu, bad)) {
-            if (bad && lane < kBlockRows) atomicAdd(&g_kv4_bad_pages, 1u);
-            if (!page_ok(a.pool, to)) continue;
-        }
-        uint8_t *db = a.pool.base + to * a.pool.page_bytes + (int64_t)hk * a.pool.head_bytes +
-                      (row0 & mask) / kBlockRows * kBlockBytes<D>;
-        // Codes: lane l has piece l % kLanes (K's pieces, then V's) of rows l / kLanes + ...
-        const int piece = lane % kLanes;
-        const int kv = piece / (kLanes / 2), at = piece % (kLanes / 2) * 16;
+    };
+    int blk = r0 / kBlockRows + warp;
+    look(blk);
+    for (; blk * kBlockRows < r1; blk += warps) {
+        const bool there = blk * kBlockRows + lane % kBlockRows >= r0 &&
+                           blk * kBlockRows + lane % kBlockRows < r1;
+        if (there && lane < kBlockRows && !(page_ok(a.pool, page) && page_ok(a.pool, to)))
+            atomicAdd(&g_kv4_bad_pages, 1u);
+        const int dst = to, from = page_ok(a.pool, page) && page_ok(a.pool, to) ? page : -1;
+        const int from_off = off;
         uint4 codes[kTimes];
-        bool there[kTimes];
+        uint32_t have = 0;
 #pragma unroll
         for (int i = 0; i < kTimes; ++i) {
-            const int r = i * kRows + lane / kLanes;
-            const int64_t place = __shfl_sync(0xffffffffu, from, r);
-            const int place_row = __shfl_sync(0xffffffffu, row, r);
-            there[i] = place >= 0;
-            if (there[i])
-                codes[i] = *reinterpret_cast<const uint4 *>(a.pool.base + place + kv * 8 * D +
-                                                            place_row * (D / 2) + at);
+            const int p = __shfl_sync(0xffffffffu, from, i * kRows + lane / kLanes);
+            const int o = __shfl_sync(0xffffffffu, from_off, i * kRows + lane / kLanes);
+            if (p >= 0) {
+                have |= 1u << i;
+                codes[i] = *reinterpret_cast<const uint4 *>(
+                    head + p * a.pool.page_bytes + o / kBlockRows * kBlockBytes<D> + code_at +
+                    o % kBlockRows * (D / 2));
+            }
         }
         uint32_t par = 0;
         float score = 0.f;
         if (from >= 0) {
-            par = *reinterpret_cast<const uint32_t *>(a.pool.base + from + 16 * D +
-                                                      lane / kBlockRows * 64 + row * 4);
-            if (lane < kBlockRows) score = a.scores[score_from];
+            par = *reinterpret_cast<const uint32_t *>(
+                head + from * a.pool.page_bytes + from_off / kBlockRows * kBlockBytes<D> + 16 * D +
+                lane / kBlockRows * 64 + from_off % kBlockRows * 4);
+            if (lane < kBlockRows)
+                score = a.scores[(((int64_t)from * a.pool.Hk + hk) << a.pool.log2_page) + from_off];
         }
+        look(blk + warps);
+        const int dst_off = blk * kBlockRows & mask;
+        uint8_t *db = head + dst * a.pool.page_bytes + dst_off / kBlockRows * kBlockBytes<D>;
 #pragma unroll
         for (int i = 0; i < kTimes; ++i)
-            if (there[i])
-                *reinterpret_cast<uint4 *>(db + kv * 8 * D +
-                                           (i * kRows + lane / kLanes) * (D / 2) + at) = codes[i];
+            if (have >> i & 1u)
+                *reinterpret_cast<uint4 *>(db + code_at + (i * kRows + lane / kLanes) * (D / 2)) =
+                    codes[i];
         if (from >= 0) {
             *reinterpret_cast<uint32_t *>(db + 16 * D + lane * 4) = par;
             if (lane < kBlockRows)
-                a.scores[((to * a.pool.Hk + hk) << a.pool.log2_page) + (mine & mask)] = score;
+                a.scores[(((int64_t)dst * a.pool.Hk + hk) << a.pool.log2_page) + dst_off + lane] =
+                    score;
         }
     }
 }
@@ -131,30 +134,36 @@ __device__ __forceinline__ void move_rows(const EvictArgs &a, int64_t b, int hk,
 // One cluster per (sequence, head).  Its blocks hold equal runs of the rows'
 // keys in shared memory.  The border (the budget-th largest key) is found in
 // three digits of 11, 11 and 10 bits: each block counts its keys by digit, and
-// each adds the blocks' counts up for itself.  (Counting the keys at or above
-// three candidates, two bits at a time, took sixteen such rounds and measured
-// 110 us where this takes less, see kEvictThreads' table in the tests' sizes.)
+// each adds a share of the bins up over the blocks.  (Counting the keys at or above
+// three candidates, two bits at a time and sixteen rounds, measured 110 us for
+// 64 sequences x 8 heads of up to 8192 rows where the digits measured 85.)
 // Then each block knows how many of its rows stay and how many stay before
 // them, lists its rows in place of their keys, and copies them.
 constexpr int kBins = 2048;
-constexpr int kEvictStatic = 3 * kBins * 4 + 1024;  // shared memory beside the keys
 
 // Words from one thread's keys to the next's: `each`, made an odd number of
 // 16-byte steps so that eight lanes' loads fall on different banks.
 __host__ __device__ __forceinline__ int key_stride(int each) { return each % 8 == 0 ? each + 4 : each; }
 
-template <int D>
-__global__ void __launch_bounds__(kEvictThreads) qkn_kv4_evict_kernel(const EvictArgs a)
+// kCluster: more than one block, each with an SM to itself and registers to
+// match; else two to an SM, whose counting and copying overlap.  (256 threads
+// and four blocks to an SM measured 115 us, 512 and three 119, with 1024 in a
+// cluster 88 us for 2 sequences of 131072 where 512 measured 63.)
+template <int D, bool kCluster>
+__global__ void __launch_bounds__(kEvictThreads, 2)
+qkn_kv4_evict_kernel(const EvictArgs a)
 {
     constexpr int kWarpsOf = kEvictThreads / 32;
     extern __shared__ __align__(16) uint32_t keys[];
-    __shared__ __align__(16) int hist[3][kBins];
+    __shared__ __align__(16) int hist[kBins];  // this block's counts of one digit
+    __shared__ __align__(16) int sums[kCluster ? kBins / 2 : 1];  // the cluster's, this block's bins
     __shared__ int warp_gt[kWarpsOf], warp_eq[kWarpsOf];
     __shared__ int block_gt, block_eq, s_digit, s_left;
     cg::cluster_group cluster = cg::this_cluster();
-    const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int blocks = kCluster ? (int)cluster.num_blocks() : 1;
+    const int rank = kCluster ? (int)cluster.block_rank() : 0;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    for (int i = tid; i < 3 * kBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < kBins; i += kEvictThreads) hist[i] = 0;
     pdl_wait_then_release();
 
     const int64_t item = blockIdx.x / blocks;
@@ -216,29 +225,37 @@ __global__ void __launch_bounds__(kEvictThreads) qkn_kv4_evict_kernel(const Evic
         const uint32_t mask = digit == 0 ? 0u : (digit == 1 ? 0xffe00000u : 0xfffffc00u);
         for (int i = 0; i < each; i += 4) {
             const uint4 k = *reinterpret_cast<const uint4 *>(mine + i);
-            if ((k.x & mask) == border) atomicAdd(&hist[digit][k.x >> shift & bins], 1);
-            if ((k.y & mask) == border) atomicAdd(&hist[digit][k.y >> shift & bins], 1);
-            if ((k.z & mask) == border) atomicAdd(&hist[digit][k.z >> shift & bins], 1);
-            if ((k.w & mask) == border) atomicAdd(&hist[digit][k.w >> shift & bins], 1);
+            if ((k.x & mask) == border) atomicAdd(&hist[k.x >> shift & bins], 1);
+            if ((k.y & mask) == border) atomicAdd(&hist[k.y >> shift & bins], 1);
+            if ((k.z & mask) == border) atomicAdd(&hist[k.z >> shift & bins], 1);
+            if ((k.w & mask) == border) atomicAdd(&hist[k.w >> shift & bins], 1);
         }
-        if (blocks > 1)
-            cluster.sync();
-        else
-            __syncthreads();
+        __syncthreads();
         // Four bins to a thread, the highest first.
         const int bin = kBins - 4 - 4 * tid;
-        int4 c = *reinterpret_cast<const int4 *>(&hist[digit][bin]);
-        if (blocks > 1) {
-            c = make_int4(0, 0, 0, 0);
-            for (int r = 0; r < blocks; ++r) {
-                const int4 x = *reinterpret_cast<const int4 *>(
-                    cluster.map_shared_rank(&hist[digit][bin], r));
-                c.x += x.x;
-                c.y += x.y;
-                c.z += x.z;
-                c.w += x.w;
+        int4 c = *reinterpret_cast<const int4 *>(&hist[bin]);
+        if constexpr (kCluster) {
+            // Each block adds up an equal share of the bins, and reads the others'.
+            const int share = kBins / blocks;
+            cluster.sync();
+            for (int i = tid * 4; i < share; i += kEvictThreads * 4) {
+                int4 x = make_int4(0, 0, 0, 0);
+#pragma unroll 8
+                for (int r = 0; r < blocks; ++r) {
+                    const int4 y = *reinterpret_cast<const int4 *>(
+                        cluster.map_shared_rank(&hist[rank * share + i], r));
+                    x.x += y.x;
+                    x.y += y.y;
+                    x.z += y.z;
+                    x.w += y.w;
+                }
+                *reinterpret_cast<int4 *>(&sums[i]) = x;
             }
+            cluster.sync();
+            c = *reinterpret_cast<const int4 *>(
+                cluster.map_shared_rank(&sums[bin % share], bin / share));
         }
+        *reinterpret_cast<int4 *>(&hist[bin]) = make_int4(0, 0, 0, 0);  // for the next digit
         const int own = c.x + c.y + c.z + c.w;
         int sum = own;
 #pragma unroll
@@ -303,7 +320,7 @@ __global__ void __launch_bounds__(kEvictThreads) qkn_kv4_evict_kernel(const Evic
         eq_all += warp_eq[w];
     }
     int gt_blocks = 0, eq_blocks = 0;  // in the blocks before this one
-    if (blocks > 1) {
+    if constexpr (kCluster) {
         if (tid == 0) {
             block_gt = gt_all;
             block_eq = eq_all;
@@ -318,7 +335,7 @@ __global__ void __launch_bounds__(kEvictThreads) qkn_kv4_evict_kernel(const Evic
     // The block's kept rows are [first, first + kept_here) of the head's.
     const int first = gt_blocks + min(eq_blocks, ties);
     const int last = gt_blocks + gt_all + min(eq_blocks + eq_all, ties);
-    // Which of the thread's rows stay (`each` is at most 96), then their list
+    // Which of the thread's rows stay (`each` is at most 80), then their list
     // in place of the keys.
     uint32_t stay[3] = {};
     int e = eq_blocks + eq_before;
@@ -336,8 +353,16 @@ __global__ void __launch_bounds__(kEvictThreads) qkn_kv4_evict_kernel(const Evic
             keys[at++] = (uint32_t)(r0 + tid * each + word * 32 + __ffs(m) - 1);
     __syncthreads();
     for (int i = tid; i < last - first; i += kEvictThreads) kept[first + i] = (int32_t)keys[i];
-    move_rows<D>(a, b, hk, first, last, warp, kWarpsOf,
-                 [&](int r) { return (int)keys[r - first]; });
+    if constexpr (kCluster) {
+        // The blocks copy equal shares: the newest rows all stay, and all lie in
+        // the last blocks' runs.  (The barrier makes the list visible.)
+        cluster.sync();
+        const int share = ((a.budget + blocks - 1) / blocks + kBlockRows - 1) / kBlockRows * kBlockRows;
+        const int m0 = min(a.budget, rank * share), m1 = min(a.budget, m0 + share);
+        move_rows<D>(a, b, hk, m0, m1, warp, kWarpsOf, [&](int r) { return __ldcg(kept + r); });
+    } else {
+        move_rows<D>(a, b, hk, first, last, warp, kWarpsOf, [&](int r) { return (int)keys[r]; });
+    }
 }
 
 // Sequences too long for a cluster's shared memory: the same choice by one

@@ -291,47 +291,32 @@ struct Attention {
 };
 
 // ---------------------------------------------------------------- eviction --
-// Rows of a head that a cluster holds at most: 96 to a thread, 8 blocks.
-constexpr int kEvictEach = 96;
+// Rows of a head that a cluster holds at most: 80 to a thread, 8 blocks.
+constexpr int kEvictEach = 80;
 constexpr int kMaxCluster = 8;
 
-template <int D>
-int run_evict(const EvictArgs &a, cudaStream_t stream)
+template <int D, bool kCluster>
+int launch_evict(const EvictArgs &a, int cluster, int64_t rows, cudaStream_t stream)
 {
     static std::atomic<int> cache[kMaxDevices];
-    auto kern = qkn_kv4_evict_kernel<D>;
-    constexpr int max_smem = (kEvictEach + 4) * kEvictThreads * 4;
-    const int64_t items = a.B * a.pool.Hk;
-    const int64_t rows = a.max_pages << a.pool.log2_page;
-    int dev = 0, sms = 0, rc;
-    if ((rc = device_sms(&sms)) != QKN_OK) return rc;
-    if (rows > (int64_t)kEvictEach * kEvictThreads * kMaxCluster) {
-        rc = launch(qkn_kv4_select_kernel, dim3((unsigned)items), kEvictThreads, 0, stream, a);
-        if (rc != QKN_OK) return rc;
-        int64_t each = (4 * (int64_t)sms + items - 1) / items;
-        if (each > a.budget / 256 + 1) each = a.budget / 256 + 1;
-        return launch(qkn_kv4_move_kernel<D>, dim3((unsigned)items, (unsigned)each), kEvictThreads,
-                      0, stream, a);
-    }
+    auto kern = qkn_kv4_evict_kernel<D, kCluster>;
+    const auto bytes = [](int each) { return key_stride(each) * kEvictThreads * 4; };
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 0 || dev >= kMaxDevices) return QKN_ERR_UNSUPPORTED;
     if (cache[dev].load(std::memory_order_acquire) == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 bytes(kEvictEach));
         if (e != cudaSuccess) return cuda_fail(e);
         cache[dev].store(1, std::memory_order_release);
     }
-    // Blocks to a head: what its rows need, and more while heads are few and
-    // each block keeps kEvictThreads * 8 rows or more.
-    int cluster = 1;
-    while (cluster < kMaxCluster &&
-           (rows > (int64_t)cluster * kEvictThreads * kEvictEach ||
-            (rows > (int64_t)cluster * kEvictThreads * 8 && items * cluster * 2 <= 2 * sms)))
-        cluster *= 2;
-    const int each = (int)((rows + cluster * kEvictThreads - 1) / (cluster * kEvictThreads) + 3) / 4 * 4;
+    const int each =
+        (int)((rows + cluster * kEvictThreads - 1) / (cluster * kEvictThreads) + 3) / 4 * 4;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * cluster));
+    cfg.gridDim = dim3((unsigned)(a.B * a.pool.Hk * cluster));
     cfg.blockDim = dim3(kEvictThreads);
-    cfg.dynamicSmemBytes = (size_t)key_stride(each) * kEvictThreads * 4;
+    cfg.dynamicSmemBytes = (size_t)bytes(each);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -345,6 +330,31 @@ int run_evict(const EvictArgs &a, cudaStream_t stream)
     e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? QKN_OK : cuda_fail(e);
+}
+
+template <int D>
+int run_evict(const EvictArgs &a, cudaStream_t stream)
+{
+    const int64_t items = a.B * a.pool.Hk;
+    const int64_t rows = a.max_pages << a.pool.log2_page;
+    int sms = 0, rc;
+    if ((rc = device_sms(&sms)) != QKN_OK) return rc;
+    if (rows > (int64_t)kEvictEach * kEvictThreads * kMaxCluster) {
+        rc = launch(qkn_kv4_select_kernel, dim3((unsigned)items), kEvictThreads, 0, stream, a);
+        if (rc != QKN_OK) return rc;
+        int64_t each = (4 * (int64_t)sms + items - 1) / items;
+        if (each > a.budget / 256 + 1) each = a.budget / 256 + 1;
+        return launch(qkn_kv4_move_kernel<D>, dim3((unsigned)items, (unsigned)each), kEvictThreads,
+                      0, stream, a);
+    }
+    // Blocks to a head: what its rows need, and more while there are SMs for
+    // them and each keeps 4096 rows or more.
+    int cluster = 1;
+    while (cluster < kMaxCluster && (rows > (int64_t)cluster * kEvictThreads * kEvictEach ||
+                                     (rows > cluster * 4096 && items * cluster * 2 <= sms)))
+        cluster *= 2;
+    return cluster > 1 ? launch_evict<D, true>(a, cluster, rows, stream)
+                       : launch_evict<D, false>(a, 1, rows, stream);
 }
 
 int attention_shape(int64_t B, int dtype, int Hq, int Hk, int D, int max_q, int64_t max_kv)
