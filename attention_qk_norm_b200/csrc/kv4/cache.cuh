@@ -49,13 +49,13 @@ __device__ __forceinline__ RowParams row_params(const float (&y)[kN])
         hi = fmaxf(hi, y[e]);
         finite = finite && fabsf(y[e]) <= 3.402823466e38f;
     }
-    // A row that is not finite spreads as NaN through the two shuffles.
-    int bad = finite ? 0 : 1;
+    const uint32_t lanes = kWidth == 32 ? 0xffffffffu
+                                        : ((1u << (kWidth % 32)) - 1u) << (threadIdx.x % 32 / kWidth * kWidth);
+    const bool bad = (__ballot_sync(0xffffffffu, !finite) & lanes) != 0;
 #pragma unroll
     for (int o = kWidth / 2; o > 0; o >>= 1) {
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        bad |= __shfl_xor_sync(0xffffffffu, bad, o);
     }
     RowParams p;
     p.step = __fmul_rn(__fsub_rn(__fmul_rn(hi, 0.5f), __fmul_rn(lo, 0.5f)), 2.0f / 15.0f);
@@ -65,12 +65,13 @@ __device__ __forceinline__ RowParams row_params(const float (&y)[kN])
     return p;
 }
 
-// Eight codes in one word, element 0 in the lowest nibble.
+// An element's code.  Adding 1.5 * 2^23 + 8 rounds to a whole number, ties to
+// even like rint, and leaves code and nothing else in the lowest 4 bits.
 __device__ __forceinline__ uint32_t row_code(float y, const RowParams &p, float inv)
 {
-    float c = rintf(__fmul_rn(__fsub_rn(y, p.mid), inv));
+    float c = __fmul_rn(__fsub_rn(y, p.mid), inv);
     c = fminf(fmaxf(c, -8.f), 7.f);  // NaN becomes -8
-    return (uint32_t)((int)c + 8);
+    return __float_as_uint(__fadd_rn(c, 12582920.f)) & 15u;
 }
 
 // {scale, mid} as stored: bf16 each, scale in the low half.
@@ -89,192 +90,272 @@ __device__ __forceinline__ void unpack_params(uint32_t w, float &scale, float &m
 constexpr int kAppendThreads = 256;
 
 // One sub-warp holds a (token, head) row, as in the per-head QK-Norm kernel,
-// and visits rows with a grid stride, kAppendRows at a time in flight.  A row
-// is read once: its sum of squares, its extremes and its codes all come from
-// the same registers.  kNorm: heads [0, Hq) queries, [Hq, Hq+Hk) keys, both
-// normalised in place, then values; otherwise the rows are the key and value
-// heads alone and nothing is written back.
-template <typename TS, int D, bool kNorm>
-__global__ void __launch_bounds__(kAppendThreads)
-qkn_kv4_append_kernel(TS *__restrict__ qkv, int64_t row_stride, int64_t T, int Hq, int Hk,
-                      const float *__restrict__ gamma_q, const float *__restrict__ gamma_k,
-                      float eps, const int64_t *__restrict__ slots, Pool pool,
-                      float *__restrict__ scores)
+// and visits rows with a grid stride, kU at a time in flight.  A row is read
+// once: its sum of squares, its extremes and its codes all come from the same
+// registers.  Blocks walk rows of one kind, so that a thread holds one weight
+// slice and runs one kind's instructions: query rows are normalised in place,
+// key rows too and stored, value rows only stored.  (One walk over all rows
+// with the kind chosen for each took 110 us for 16384 tokens of 32q/8kv x 128
+// bf16.)
+enum RowKind { kQueryRows, kKeyRows, kValueRows };
+
+// Lanes to a row: one 16-byte vector to a lane for query rows; for stored
+// rows, whose extremes, slot and parameters are work for each lane, two (FP8's
+// vectors are 16 elements: one).  (The sum of squares keeps the per-head
+// kernel's order either way: a lane's two vectors are the ones that its first
+// shuffle would have added.)
+template <typename TS, int D, bool kStored>
+constexpr int kAppendLanes = D / Storage<TS>::kVec > 32  ? 32
+                             : kStored && Storage<TS>::kVec <= 8 ? D / Storage<TS>::kVec / 2
+                                                                     : D / Storage<TS>::kVec;
+template <typename TS, int D, bool kStored>
+constexpr int kAppendRows = D / kAppendLanes<TS, D, kStored> > 8 ? 1 : 2;
+
+template <typename TS, int D, bool kNorm, RowKind kKind>
+__device__ __forceinline__ void append_rows(TS *__restrict__ qkv, int64_t row_stride, int64_t T,
+                                            int first, int heads,
+                                            const float *__restrict__ gamma, float eps,
+                                            const int64_t *__restrict__ slots, const Pool &pool,
+                                            float *__restrict__ scores, int block, int blocks)
 {
     using S = Storage<TS>;
     constexpr int kVec = S::kVec;
     constexpr int kNV = D / kVec;
-    constexpr int kLPR = kNV < 32 ? kNV : 32;
+    constexpr int kLPR = kAppendLanes<TS, D, kKind != kQueryRows>;
     constexpr int kVPL = kNV / kLPR;
     constexpr int kEPL = kVPL * kVec;
+    constexpr int kU = kAppendRows<TS, D, kKind != kQueryRows>;
+    constexpr bool kPairs = kVPL == 2 && kNV <= 32;  // the first shuffle's sum in the lane
     constexpr bool kPacked = kVec == 16;  // the per-head kernel's order of sums
-    pdl_wait_then_release();
+    constexpr bool kScale = kNorm && kKind != kValueRows;
 
-    const int heads = kNorm ? Hq + 2 * Hk : 2 * Hk;
-    const int first = kNorm ? 0 : Hq;
-    const uint64_t tid = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const uint64_t tid = (uint64_t)block * kAppendThreads + threadIdx.x;
     const int lane = (int)(tid % kLPR);
-    const uint64_t groups = (uint64_t)gridDim.x * blockDim.x / kLPR;
-    const uint64_t rows = (uint64_t)T * heads;
-    int64_t t = (int64_t)((tid / kLPR) / heads);
-    int h = (int)((tid / kLPR) - (uint64_t)t * heads) + first;
-    const int64_t dt = (int64_t)(groups / heads);
-    const int dh = (int)(groups - (uint64_t)dt * heads);
+    const uint64_t groups = (uint64_t)blocks * (kAppendThreads / kLPR);
+    const uint64_t rows = (uint64_t)T * heads, step = groups * kU;
+    int64_t t[kU];
+    int h[kU];
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+        const uint64_t r = tid / kLPR + k * groups;
+        t[k] = (int64_t)(r / heads);
+        h[k] = (int)(r - (uint64_t)t[k] * heads);
+    }
+    const int64_t dt = (int64_t)(step / heads);
+    const int dh = (int)(step - (uint64_t)dt * heads);
+    float g[kScale ? kEPL : 1];
+    if constexpr (kScale) {
+#pragma unroll
+        for (int v = 0; v < kVPL; ++v) {
+            float x[kVec];
+            load_gamma<kVec>(gamma + (lane + v * kLPR) * kVec, x);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) g[v * kVec + e] = x[e];
+        }
+    }
 
     // Whole warps take each step together (the shuffles need every lane).
-    for (uint64_t base = 0; base < rows; base += groups) {
-        const bool live = t < T;
-        const bool is_q = kNorm && h < Hq;
-        const bool is_v = h >= Hq + Hk;
-        uint4 *ptr = reinterpret_cast<uint4 *>(qkv + t * row_stride + (int64_t)h * D) + lane;
-        float f[kVPL][kVec];
+    for (uint64_t base = 0; base < rows; base += step) {
+        uint4 x[kU][kVPL];
+        uint4 *ptr[kU];
+        int64_t slot[kU];
 #pragma unroll
-        for (int v = 0; v < kVPL; ++v)
-            S::unpack(live ? load_stream(ptr + v * kLPR) : zero_vec<uint4>(), f[v]);
-        float rinv = 1.f;
-        float y[kEPL];
+        for (int k = 0; k < kU; ++k) {
+            const bool live = t[k] < T;
+            ptr[k] = reinterpret_cast<uint4 *>(qkv + t[k] * row_stride +
+                                               (int64_t)(first + h[k]) * D) + lane;
 #pragma unroll
-        for (int v = 0; v < kVPL; ++v)
+            for (int v = 0; v < kVPL; ++v)
+                x[k][v] = live ? load_stream(ptr[k] + v * kLPR) : zero_vec<uint4>();
+            slot[k] = -1;
+            if (kKind != kQueryRows && live) slot[k] = slots[t[k]];
+        }
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) y[v * kVec + e] = f[v][e];
-        if constexpr (kNorm) {
-            float s = 0.f;
-            if constexpr (kPacked) {
-                uint64_t acc = f2_pack(0.f, 0.f);
+        for (int k = 0; k < kU; ++k) {
+            float f[kVPL][kVec], y[kEPL];
+            float rinv = 1.f;
 #pragma unroll
-                for (int v = 0; v < kVPL; ++v) sumsq_acc(acc, f[v]);
-                s = sumsq_total(acc);
+            for (int v = 0; v < kVPL; ++v) S::unpack(x[k][v], f[v]);
+            if constexpr (kScale) {
+                float s = 0.f;
+#pragma unroll
+                for (int v = 0; v < kVPL; ++v) {
+                    float part = kPairs ? 0.f : s;
+                    if constexpr (kPacked) {
+                        uint64_t acc = f2_pack(0.f, 0.f);
+                        sumsq_acc(acc, f[v]);
+                        part = sumsq_total(acc);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kVec; ++e) part = fmaf(f[v][e], f[v][e], part);
+                    }
+                    s = kPairs ? s + part : part;
+                }
+                rinv = rsqrtf(group_sum<kLPR>(s) / (float)D + eps);
+#pragma unroll
+                for (int v = 0; v < kVPL; ++v) {
+                    float o[kVec];
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) {
+                        o[e] = __fmul_rn(__fmul_rn(f[v][e], rinv), g[v * kVec + e]);
+                        y[v * kVec + e] = __fmul_rn(f[v][e], g[v * kVec + e]);
+                    }
+                    if (t[k] < T) store_stream(ptr[k] + v * kLPR, S::pack(o));
+                }
             } else {
 #pragma unroll
                 for (int v = 0; v < kVPL; ++v)
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) s = fmaf(f[v][e], f[v][e], s);
+                    for (int e = 0; e < kVec; ++e) y[v * kVec + e] = f[v][e];
             }
-            s = group_sum<kLPR>(s);
-            if (!is_v) {
-                rinv = rsqrtf(s / (float)D + eps);
-                const float *gamma = is_q ? gamma_q : gamma_k;
+            if constexpr (kKind != kQueryRows) {
+                const RowParams p = row_params<kLPR, kEPL>(y);
+                const int64_t page = slot[k] >> pool.log2_page;
+                if (slot[k] >= 0 && page < pool.pages) {
+                    constexpr int kv = kKind == kValueRows ? 1 : 0;
+                    const int off = (int)(slot[k] & ((1 << pool.log2_page) - 1));
+                    uint8_t *blk = pool.base + page * pool.page_bytes +
+                                   (int64_t)h[k] * pool.head_bytes +
+                                   off / kBlockRows * kBlockBytes<D>;
+                    const int row = off % kBlockRows;
+                    const float inv = p.step > 0.f ? __fdiv_rn(1.f, p.step) : 0.f;
+                    uint8_t *codes = blk + kv * 8 * D + row * (D / 2);
 #pragma unroll
-                for (int v = 0; v < kVPL; ++v) {
-                    float g[kVec], o[kVec];
-                    load_gamma<kVec>(gamma + (lane + v * kLPR) * kVec, g);
+                    for (int v = 0; v < kVPL; ++v) {
+                        uint32_t w[(kVec + 7) / 8] = {};
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) {
-                        o[e] = __fmul_rn(__fmul_rn(f[v][e], rinv), g[e]);
-                        y[v * kVec + e] = __fmul_rn(f[v][e], g[e]);
+                        for (int e = 0; e < kVec; ++e)
+                            w[e / 8] |= row_code(y[v * kVec + e], p, inv) << (4 * (e % 8));
+                        uint8_t *at = codes + (lane + v * kLPR) * (kVec / 2);
+                        if constexpr (kVec == 4)
+                            *reinterpret_cast<uint16_t *>(at) = (uint16_t)w[0];
+                        else if constexpr (kVec == 8)
+                            *reinterpret_cast<uint32_t *>(at) = w[0];
+                        else
+                            *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
                     }
-                    if (live) store_stream(ptr + v * kLPR, S::pack(o));
+                    if (lane == 0) {
+                        *reinterpret_cast<uint32_t *>(blk + 16 * D + kv * 64 + row * 4) =
+                            pack_params(p.step * rinv, p.mid * rinv);
+                        if (scores != nullptr && kv == 0)
+                            scores[((page * pool.Hk + h[k]) << pool.log2_page) + off] = 0.f;
+                    }
+                } else if (slot[k] >= 0 && lane == 0) {
+                    atomicAdd(&g_kv4_bad_pages, 1u);
                 }
             }
-        }
-        // Extremes over the sub-warp: every lane takes part, query rows too.
-        RowParams p = row_params<kLPR, kEPL>(y);
-        if (live && !is_q) {
-            const int64_t slot = slots[t];
-            const int64_t page = slot >> pool.log2_page;
-            if (slot >= 0 && page < pool.pages) {
-                const int kv = is_v ? 1 : 0;
-                const int hk = h - Hq - kv * Hk;
-                const int off = (int)(slot & ((1 << pool.log2_page) - 1));
-                uint8_t *blk = pool.base + page * pool.page_bytes +
-                               (int64_t)hk * pool.head_bytes +
-                               (off / kBlockRows) * kBlockBytes<D>;
-                const int row = off % kBlockRows;
-                const float inv = p.step > 0.f ? __fdiv_rn(1.f, p.step) : 0.f;
-                uint8_t *codes = blk + kv * 8 * D + row * (D / 2);
-#pragma unroll
-                for (int v = 0; v < kVPL; ++v) {
-                    uint32_t w[(kVec + 7) / 8] = {};
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e)
-                        w[e / 8] |= row_code(y[v * kVec + e], p, inv) << (4 * (e % 8));
-                    uint8_t *at = codes + (lane + v * kLPR) * (kVec / 2);
-                    if constexpr (kVec == 4)
-                        *reinterpret_cast<uint16_t *>(at) = (uint16_t)w[0];
-                    else if constexpr (kVec == 8)
-                        *reinterpret_cast<uint32_t *>(at) = w[0];
-                    else
-                        *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
-                }
-                if (lane == 0) {
-                    *reinterpret_cast<uint32_t *>(blk + 16 * D + kv * 64 + row * 4) =
-                        pack_params(p.step * rinv, p.mid * rinv);
-                    if (scores != nullptr && kv == 0)
-                        scores[((page * pool.Hk + hk) << pool.log2_page) + off] = 0.f;
-                }
-            } else if (slot >= 0 && lane == 0) {
-                atomicAdd(&g_kv4_bad_pages, 1u);
+            t[k] += dt;
+            h[k] += dh;
+            if (h[k] >= heads) {
+                h[k] -= heads;
+                t[k] += 1;
             }
-        }
-        t += dt;
-        h += dh;
-        if (h >= heads + first) {
-            h -= heads;
-            t += 1;
         }
     }
 }
 
+// q_blocks, then k_blocks, then the value rows' blocks.
+template <typename TS, int D, bool kNorm>
+__global__ void __launch_bounds__(kAppendThreads)
+qkn_kv4_append_kernel(TS *__restrict__ qkv, int64_t row_stride, int64_t T, int Hq, int Hk,
+                      const float *__restrict__ gamma_q, const float *__restrict__ gamma_k,
+                      float eps, const int64_t *__restrict__ slots, const Pool pool,
+                      float *__restrict__ scores, int q_blocks, int k_blocks)
+{
+    pdl_wait_then_release();
+    const int block = blockIdx.x;
+    if (kNorm && block < q_blocks)
+        append_rows<TS, D, kNorm, kQueryRows>(qkv, row_stride, T, 0, Hq, gamma_q, eps, slots, pool,
+                                              scores, block, q_blocks);
+    else if (block < q_blocks + k_blocks)
+        append_rows<TS, D, kNorm, kKeyRows>(qkv, row_stride, T, Hq, Hk, gamma_k, eps, slots, pool,
+                                            scores, block - q_blocks, k_blocks);
+    else
+        append_rows<TS, D, kNorm, kValueRows>(qkv, row_stride, T, Hq + Hk, Hk, nullptr, eps, slots,
+                                              pool, scores, block - q_blocks - k_blocks,
+                                              (int)gridDim.x - q_blocks - k_blocks);
+}
+
 // ------------------------------------------------------------------- read --
-// One sub-warp per (slot, head, K or V) row: kVec elements of the output type
-// to a lane.
+// A sub-warp to a (slot, head, K or V) row, two 16-byte vectors of the output
+// to a lane (four in fp32 at D = 256): a row's slot, page and parameters are
+// work for each lane, and one vector to a lane was bound by it.
+template <typename TS, int D>
+constexpr int kReadLanes = D / Storage<TS>::kVec < 4 ? D / Storage<TS>::kVec
+                                                     : (D / Storage<TS>::kVec >= 64
+                                                            ? 16
+                                                            : D / Storage<TS>::kVec / 2);
 template <typename TS, int D>
 __global__ void __launch_bounds__(kAppendThreads)
-qkn_kv4_read_kernel(Pool pool, const int64_t *__restrict__ slots, int64_t N,
+qkn_kv4_read_kernel(const Pool pool, const int64_t *__restrict__ slots, int64_t N,
                     TS *__restrict__ k, TS *__restrict__ v, int64_t row_stride)
 {
     using S = Storage<TS>;
     constexpr int kVec = S::kVec;
-    constexpr int kNV = D / kVec;
-    constexpr int kLPR = kNV < 32 ? kNV : 32;
-    constexpr int kVPL = kNV / kLPR;
+    constexpr int kLPR = kReadLanes<TS, D>;
+    constexpr int kVPL = D / kVec / kLPR;
     pdl_wait_then_release();
     const uint64_t tid = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int lane = (int)(tid % kLPR);
     const uint64_t groups = (uint64_t)gridDim.x * blockDim.x / kLPR;
-    const uint64_t rows = (uint64_t)N * 2 * pool.Hk;
-    for (uint64_t r = tid / kLPR; r < rows; r += groups) {
-        const int64_t i = (int64_t)(r / (2 * pool.Hk));
-        const int part = (int)(r - (uint64_t)i * 2 * pool.Hk);
+    const int heads = 2 * pool.Hk;  // K's, then V's
+    int64_t i = (int64_t)(tid / kLPR / heads);
+    int part = (int)(tid / kLPR - (uint64_t)i * heads);
+    const int64_t di = (int64_t)(groups / heads);
+    const int dpart = (int)(groups - (uint64_t)di * heads);
+    while (i < N) {
         const int kv = part >= pool.Hk ? 1 : 0;
         const int hk = part - kv * pool.Hk;
         TS *out = kv ? v : k;
-        if (out == nullptr) continue;
-        const int64_t slot = slots[i];
-        const int64_t page = slot >> pool.log2_page;
-        const bool ok = slot >= 0 && page < pool.pages;
-        const int off = (int)(slot & ((1 << pool.log2_page) - 1));
-        const uint8_t *blk = pool.base + (ok ? page : 0) * pool.page_bytes +
-                             (int64_t)hk * pool.head_bytes + (off / kBlockRows) * kBlockBytes<D>;
-        const int row = off % kBlockRows;
-        float scale = 0.f, mid = 0.f;
-        if (ok)
-            unpack_params(*reinterpret_cast<const uint32_t *>(blk + 16 * D + kv * 64 + row * 4),
-                          scale, mid);
-        else if (slot >= 0 && lane == 0 && hk == 0)
-            atomicAdd(&g_kv4_bad_pages, 1u);
-        const uint8_t *codes = blk + kv * 8 * D + row * (D / 2);
-        uint4 *to = reinterpret_cast<uint4 *>(out + i * row_stride + (int64_t)hk * D);
+        if (out != nullptr) {
+            const int64_t slot = slots[i];
+            const int64_t page = slot >> pool.log2_page;
+            uint32_t w[kVPL][(kVec + 7) / 8] = {};
+            uint32_t par = 0;
+            if (slot >= 0 && page < pool.pages) {
+                const int off = (int)(slot & ((1 << pool.log2_page) - 1));
+                const uint8_t *blk = pool.base + page * pool.page_bytes +
+                                     (int64_t)hk * pool.head_bytes +
+                                     off / kBlockRows * kBlockBytes<D>;
+                const int row = off % kBlockRows;
+                par = *reinterpret_cast<const uint32_t *>(blk + 16 * D + kv * 64 + row * 4);
+                blk += kv * 8 * D + row * (D / 2) + lane * (kVec / 2);
 #pragma unroll
-        for (int j = 0; j < kVPL; ++j) {
-            uint32_t w[(kVec + 7) / 8] = {};
-            const uint8_t *at = codes + (lane + j * kLPR) * (kVec / 2);
-            if (ok) {
-                if constexpr (kVec == 4) {
-                    w[0] = *reinterpret_cast<const uint16_t *>(at);
-                } else if constexpr (kVec == 8) {
-                    w[0] = *reinterpret_cast<const uint32_t *>(at);
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2 *>(at);
-                    w[0] = u.x;
-                    w[1] = u.y;
+                for (int j = 0; j < kVPL; ++j) {
+                    const uint8_t *at = blk + j * kLPR * (kVec / 2);
+                    if constexpr (kVec == 4) {
+                        w[j][0] = *reinterpret_cast<const uint16_t *>(at);
+                    } else if constexpr (kVec == 8) {
+                        w[j][0] = *reinterpret_cast<const uint32_t *>(at);
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                        w[j][0] = x.x;
+                        w[j][1] = x.y;
+                    }
                 }
+            } else if (slot >= 0 && lane == 0 && hk == 0) {
+                atomicAdd(&g_kv4_bad_pages, 1u);
             }
-            float f[kVec];
+            float scale, mid;
+            unpack_params(par, scale, mid);
+            uint4 *to = reinterpret_cast<uint4 *>(out + i * row_stride + (int64_t)hk * D) + lane;
 #pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                f[e] = fmaf(scale, (float)((int)((w[e / 8] >> (4 * (e % 8))) & 15u) - 8), mid);
-            store_stream(to + lane + j * kLPR, S::pack(f));
+            for (int j = 0; j < kVPL; ++j) {
+                float f[kVec];
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    // 2^23 + c, less 2^23 + 8.
+                    const uint32_t c = w[j][e / 8] >> (4 * (e % 8)) & 15u;
+                    f[e] = fmaf(scale, __uint_as_float(c | 0x4b000000u) - 8388616.f, mid);
+                }
+                store_stream(to + j * kLPR, S::pack(f));
+            }
+        }
+        i += di;
+        part += dpart;
+        if (part >= heads) {
+            part -= heads;
+            i += 1;
         }
     }
 }

@@ -142,20 +142,60 @@ int stream_grid(uint64_t groups, int lanes, int per_sm, unsigned *grid)
     return QKN_OK;
 }
 
+// Resident blocks of a kernel on an SM, looked up once for each device with
+// its shared-memory limit raised.
+template <typename Kern>
+int blocks_per_sm(Kern kern, int threads, int smem, std::atomic<int> *cache, int *out)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 0 || dev >= kMaxDevices) return QKN_ERR_UNSUPPORTED;
+    int n = cache[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+        if (smem > 0)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (n < 1) return QKN_ERR_UNSUPPORTED;
+        cache[dev].store(n, std::memory_order_release);
+    }
+    *out = n;
+    return QKN_OK;
+}
+
 struct Append {
     template <typename TS, int D>
     static int run(void *qkv, int64_t T, int Hq, int Hk, int64_t row_stride, const float *gq,
                    const float *gk, float eps, const int64_t *slots, Pool pool, float *scores,
                    bool norm, cudaStream_t stream)
     {
-        constexpr int kNV = D / Storage<TS>::kVec;
-        unsigned grid = 0;
-        const uint64_t rows = (uint64_t)T * (uint64_t)(norm ? Hq + 2 * Hk : 2 * Hk);
-        const int rc = stream_grid(rows, kNV < 32 ? kNV : 32, 6, &grid);
-        if (rc != QKN_OK) return rc;
+        // Blocks to the kinds of rows: what each fills, or shares of the
+        // resident blocks by what a row of the kind moves and computes.
+        constexpr int kPerBlock[2] = {
+            kAppendThreads / kAppendLanes<TS, D, false> * kAppendRows<TS, D, false>,
+            kAppendThreads / kAppendLanes<TS, D, true> * kAppendRows<TS, D, true>};
         auto kern = norm ? qkn_kv4_append_kernel<TS, D, true> : qkn_kv4_append_kernel<TS, D, false>;
-        return launch(kern, dim3(grid), kAppendThreads, 0, stream, static_cast<TS *>(qkv),
-                      row_stride, T, Hq, Hk, gq, gk, eps, slots, pool, scores);
+        static std::atomic<int> cache[2][kMaxDevices];
+        int sms = 0, per_sm = 0, rc;
+        if ((rc = device_sms(&sms)) != QKN_OK) return rc;
+        if ((rc = blocks_per_sm(kern, kAppendThreads, 0, cache[norm], &per_sm)) != QKN_OK) return rc;
+        const int64_t cap = (int64_t)sms * per_sm;
+        const double weight[3] = {norm ? 2.0 * Hq : 0.0, (norm ? 3.0 : 2.0) * Hk, 2.0 * Hk};
+        const int64_t rows[3] = {norm ? T * Hq : 0, T * Hk, T * Hk};
+        const double all = weight[0] + weight[1] + weight[2];
+        int64_t blocks[3], sum = 0;
+        for (int i = 0; i < 3; ++i)
+            sum += blocks[i] = (rows[i] + kPerBlock[i > 0] - 1) / kPerBlock[i > 0];
+        if (sum > cap)
+            for (int i = 0; i < 3; ++i) {
+                const int64_t share = (int64_t)(cap * weight[i] / all);
+                if (blocks[i] > share) blocks[i] = rows[i] > 0 && share < 1 ? 1 : share;
+            }
+        return launch(kern, dim3((unsigned)(blocks[0] + blocks[1] + blocks[2])), kAppendThreads, 0,
+                      stream, static_cast<TS *>(qkv), row_stride, T, Hq, Hk, gq, gk, eps, slots,
+                      pool, scores, (int)blocks[0], (int)blocks[1]);
     }
 };
 
@@ -164,9 +204,8 @@ struct Read {
     static int run(Pool pool, const int64_t *slots, int64_t N, void *k, void *v,
                    int64_t row_stride, cudaStream_t stream)
     {
-        constexpr int kNV = D / Storage<TS>::kVec;
         unsigned grid = 0;
-        const int rc = stream_grid((uint64_t)N * 2 * pool.Hk, kNV < 32 ? kNV : 32, 8, &grid);
+        const int rc = stream_grid((uint64_t)N * 2 * pool.Hk, kReadLanes<TS, D>, 8, &grid);
         if (rc != QKN_OK) return rc;
         return launch(qkn_kv4_read_kernel<TS, D>, dim3(grid), kAppendThreads, 0, stream, pool,
                       slots, N, static_cast<TS *>(k), static_cast<TS *>(v), row_stride);
@@ -226,28 +265,6 @@ AttentionPlan attention_plan(int64_t B, int dtype, int Hq, int Hk, int D, int ma
     return p;
 }
 
-// Resident blocks of a kernel on an SM, looked up once for each device with
-// its shared-memory limit raised.
-template <typename Kern>
-int blocks_per_sm(Kern kern, int smem, std::atomic<int> *cache, int *out)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (dev < 0 || dev >= kMaxDevices) return QKN_ERR_UNSUPPORTED;
-    int n = cache[dev].load(std::memory_order_acquire);
-    if (n == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem);
-        if (e != cudaSuccess) return cuda_fail(e);
-        if (n < 1) return QKN_ERR_UNSUPPORTED;
-        cache[dev].store(n, std::memory_order_release);
-    }
-    *out = n;
-    return QKN_OK;
-}
-
 template <typename TS, int D, int NT, bool kScores>
 int launch_attention(const AttentionArgs &a, const AttentionPlan &p, cudaStream_t stream)
 {
@@ -256,7 +273,7 @@ int launch_attention(const AttentionArgs &a, const AttentionPlan &p, cudaStream_
     auto kern = qkn_kv4_attention_kernel<TS, D, NT, kScores>;
     int per_sm = 0, sms = 0, rc;
     if ((rc = device_sms(&sms)) != QKN_OK) return rc;
-    if ((rc = blocks_per_sm(kern, smem, cache, &per_sm)) != QKN_OK) return rc;
+    if ((rc = blocks_per_sm(kern, kThreads, smem, cache, &per_sm)) != QKN_OK) return rc;
     if (p.direct)
         return launch(kern, dim3((unsigned)(a.B * (int64_t)p.max_items)), kThreads, smem, stream, a);
     const int64_t units = (int64_t)a.B * p.max_items * p.max_units;
