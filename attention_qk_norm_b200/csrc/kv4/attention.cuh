@@ -309,10 +309,9 @@ template <>
 constexpr int kWeightParts<__nv_bfloat16> = 1;
 template <>
 constexpr int kWeightParts<__nv_fp8_e4m3> = 1;
-// Values as raw codes: each 16 rows' sums get -8 times their weights from a
-// product with a constant operand, which costs a matrix instruction where the
-// subtraction from four operand registers would cost four others.  That pays
-// while there is one query tile and one part.
+// Values as raw codes: a unit's sums get -8 times its weights on fp32 pairs,
+// D/8 instructions where centring the operands takes D/2.  That pays while
+// there is one query tile and one part.
 template <typename TS, int NT>
 constexpr bool kRawValues = NT == 1 && kWeightParts<TS> == 1;
 
@@ -797,7 +796,27 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                             wf[half][nt][part][r] = transpose8x8(wf[half][nt][part][r]);
 
             // O^T += V^T W^T: operand rows g and g + 8 of m-tile 4 * v + p are
-            // elements p and p + 4 of the lane's word v.
+            // elements p and p + 4 of the lane's word v.  With raw codes, 8 times
+            // the unit's weights are taken off every sum: their own sums come
+            // from a product with ones.
+            if constexpr (kRawV) {
+                float y[4] = {};
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    mma(y, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, wf[half][0][0][0],
+                        wf[half][0][0][1]);
+                // As large as a raw code is: 2^-24 in even tiles, 2^-20 in odd ones.
+                const uint64_t even = f2_pack(-8.f / 16777216.f, -8.f / 16777216.f);
+                const uint64_t odd = f2_pack(-8.f / 1048576.f, -8.f / 1048576.f);
+                const uint64_t yy = f2_pack(y[0], y[1]);
+#pragma unroll
+                for (int mt = 0; mt < kMTiles; ++mt)
+#pragma unroll
+                    for (int c = 0; c < 4; c += 2)
+                        f2_unpack(f2_fma(yy, mt % 2 ? odd : even,
+                                         f2_pack(acc[mt][0][c], acc[mt][0][c + 1])),
+                                  acc[mt][0][c], acc[mt][0][c + 1]);
+            }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const uint8_t *blk = unit + half * kBB + 8 * D + g * (D / 16);
@@ -835,15 +854,6 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                                 const uint32_t b0 = wf[half][nt][part][0], b1 = wf[half][nt][part][1];
                                 mma(acc[4 * v + p][nt], x0[p], x1[p], x2[p], x3[p], b0, b1);
                             }
-                    if constexpr (kRawV) {
-#pragma unroll
-                        for (int p = 0; p < 4; ++p) {
-                            // -8, as large as the tile's raw codes are.
-                            const uint32_t c = p % 2 ? 0x80808080u : 0x80088008u;
-                            mma(acc[4 * v + p][0], c, c, c, c, wf[half][0][0][0],
-                                wf[half][0][0][1]);
-                        }
-                    }
                 }
             }
         };
