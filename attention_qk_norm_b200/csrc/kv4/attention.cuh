@@ -32,11 +32,11 @@ namespace {
 // What a block of the attention kernel leaves for the kernels behind it: its
 // run of units, and the split item that begins in it (join_b < 0: none).
 struct RunRecord {
-    int64_t first, all;      // first unit, and all units of the call
-    int total;               // units of the run
-    int b, item, unit;       // where it begins
-    int join_b, join_item;   // the item
+    uint32_t first, total;     // first unit, units
+    int b, item, unit;         // where it begins
+    int join_b, join_item;     // the item
     int join_slot, join_last;  // its part here, and the last block that holds one
+    int pad[3];
 };
 
 struct AttentionArgs {
@@ -55,8 +55,9 @@ struct AttentionArgs {
     float *lse;
     float *scores;
     // Launch shape and workspace.
-    int direct;        // one block per item, no item is split
-    int max_items;     // items of a sequence at most (direct)
+    int max_units;     // units of an item at most
+    int zones[4];      // where each row of blocks begins in the units, in 128ths
+    int max_items;     // items of a sequence at most
     int log_rows;      // query rows of a logit record
     RunRecord *runs;   // [blocks]
     float *part;       // [2 * blocks][rows][D]: sums of items split over blocks
@@ -98,8 +99,8 @@ __device__ __forceinline__ void q_range(const AttentionArgs &a, int b, int &star
 // end among them ends behind them.
 constexpr int kUnitRows = 32;
 constexpr int kItemUnits = 4;
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
+constexpr int kRunWarps = 4;  // of a block that takes a run of units
+constexpr int kRunThreads = kRunWarps * 32;
 
 struct Seq {
     int n, start, count;  // cached rows, first query token, query tokens
@@ -145,60 +146,101 @@ struct Walk {
     }
 };
 
-// The block's run of units [first, first + count) and where it begins; also
-// all sequences' units before sequence w.b.  Every block adds the lengths up
-// for itself (B numbers from L2).
+// The blocks' runs.  The grid is the resident blocks, a row of it (y) one block
+// on every SM, started in this order, and an SM's schedulers prefer the warps
+// that started first: with equal runs the rows' blocks ended after 75, 82, 91
+// and 99 us of a call, the SM half empty towards the end.  So a row's share of
+// the units falls with y (a.zones); its blocks share it equally.  Calls of a
+// few units a block are split equally among all blocks.
+constexpr uint32_t kEvenUnits = 12;
+
+struct Runs {
+    uint32_t total, blocks;
+    bool even;
+    __device__ __forceinline__ Runs(uint32_t units)
+    {
+        total = units;
+        blocks = gridDim.x * gridDim.y;
+        even = gridDim.y == 1 || units < kEvenUnits * blocks;
+    }
+    __device__ __forceinline__ uint32_t zone(const AttentionArgs &a, uint32_t y) const
+    {
+        return y < gridDim.y ? (uint32_t)((uint64_t)total * (uint32_t)a.zones[y] >> 7) : total;
+    }
+    // First unit of block x of row y (x == gridDim.x: of the next row).
+    __device__ __forceinline__ uint32_t begin(const AttentionArgs &a, uint32_t x, uint32_t y) const
+    {
+        const uint32_t from = even ? 0 : zone(a, y), n = even ? total : zone(a, y + 1) - from;
+        const uint32_t among = even ? blocks : gridDim.x, id = even ? y * gridDim.x + x : x;
+        const uint32_t each = n / among, rest = n - each * among;
+        return from + id * each + min(id, rest);
+    }
+    // The block whose run holds unit u.
+    __device__ __forceinline__ uint32_t holder(const AttentionArgs &a, uint32_t u) const
+    {
+        uint32_t y = 0, from = 0, n = total, among = blocks;
+        if (!even) {
+            while (y + 1 < gridDim.y && u >= zone(a, y + 1)) ++y;
+            from = zone(a, y);
+            n = zone(a, y + 1) - from;
+            among = gridDim.x;
+        }
+        u -= from;
+        const uint32_t each = n / among, rest = n - each * among;
+        const uint32_t id = u < rest * (each + 1) ? u / (each + 1) : rest + (u - rest * (each + 1)) / each;
+        return y * gridDim.x + id;
+    }
+};
+
+// This block's run [first, first + count) and where it begins; returns all
+// units of the call.  Every block adds the lengths up for itself (B numbers
+// from L2).  A run's end that falls among the empty units of an item moves
+// behind them.
 template <int kR>
-__device__ __forceinline__ int64_t block_run(const AttentionArgs &a, int64_t *scan, Walk<kR> &w,
-                                             int64_t &first, int &count)
+__device__ __forceinline__ uint32_t block_run(const AttentionArgs &a, uint32_t *scan, Walk<kR> &w,
+                                              uint32_t &first, int &count)
 {
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int per = (a.B + kThreads - 1) / kThreads;
+    const int per = (a.B + kRunThreads - 1) / kRunThreads;
     const int b0 = tid * per, b1 = min(a.B, b0 + per);
-    int64_t mine = 0;
+    uint32_t mine = 0;
     for (int b = b0; b < b1; ++b) {
         const Seq s = load_seq<kR>(a, b);
-        mine += (int64_t)s.items * s.units;
+        mine += (uint32_t)s.items * (uint32_t)s.units;
     }
-    int64_t sum = mine;
+    uint32_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+        const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += up;
     }
     if (lane == 31) scan[warp] = sum;
     __syncthreads();
-    int64_t before = 0, total = 0;
+    uint32_t before = 0, total = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < kRunWarps; ++i) {
         if (i < warp) before += scan[i];
         total += scan[i];
     }
     before += sum - mine;
-    // The run's two ends: scan[4..5] the sequence of the first and the units
-    // before it, scan[6..7] the ends, moved behind the empty units of the item
-    // that they fall among.
-    // At most as many blocks as units take part.
-    const int64_t blocks = total < gridDim.x ? total : gridDim.x;
-    const bool part = blockIdx.x < blocks;
-#pragma unroll
+    // scan[4], [5]: the first unit's sequence, and the units before it; [6],
+    // [7]: the run's ends.
+    const Runs runs(total);
+#pragma unroll 1
     for (int side = 0; side < 2; ++side) {
-        const int64_t at = part ? total * (blockIdx.x + side) / blocks : total;
+        const uint32_t at = runs.begin(a, blockIdx.x + side, blockIdx.y);
         if (at >= before && at < before + mine) {
-            int64_t seen = before;
+            uint32_t seen = before;
             int b = b0;
             Seq s = load_seq<kR>(a, b);
             for (;; s = load_seq<kR>(a, ++b)) {  // ends: `at` lies in one of these sequences
-                const int64_t u = (int64_t)s.items * s.units;
+                const uint32_t u = (uint32_t)s.items * (uint32_t)s.units;
                 if (at < seen + u) break;
                 seen += u;
             }
-            const int64_t in = at - seen;
-            const int64_t item = (uint32_t)(in >> 32) == 0 ? (uint32_t)in / (uint32_t)s.units
-                                                           : in / s.units;
-            const int unit = (int)(in - item * s.units);
-            const bool move = unit >= s.units - kItemUnits && unit > 0;
-            scan[6 + side] = move ? at + s.units - unit : at;
+            const int unit = (int)((at - seen) % (uint32_t)s.units);
+            scan[6 + side] =
+                unit >= s.units - kItemUnits && unit > 0 ? at + (s.units - unit) : at;
             if (side == 0) {
                 scan[4] = b;
                 scan[5] = seen;
@@ -214,9 +256,9 @@ __device__ __forceinline__ int64_t block_run(const AttentionArgs &a, int64_t *sc
     if (count <= 0) return total;
     w.b = (int)scan[4];
     w.load(a);
-    const int64_t in = first - scan[5];
-    w.item = (uint32_t)(in >> 32) == 0 ? (uint32_t)in / (uint32_t)w.units : (int)(in / w.units);
-    w.unit = (int)(in - (int64_t)w.item * w.units);
+    const uint32_t in = first - scan[5];
+    w.item = (int)(in / (uint32_t)w.units);
+    w.unit = (int)(in - (uint32_t)w.item * w.units);
     if (w.item >= w.items) {  // moved behind the sequence's last item
         w.item = 0;
         do {
@@ -257,7 +299,11 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
 // fp16 operands, in one of two forms.
 // Raw: the nibbles where they lie, read as subnormal numbers: c * 2^-24 for
 // even p and c * 2^-20 for odd p.  One logic instruction a pair; the power of
-// two and the 8 are made up for elsewhere.
+// two and the 8 are made up for elsewhere.  The matrix unit aligns its sums by
+// the subnormal's exponent field, 2^-14, so they keep 2^-13 of a code step
+// times the other operand's largest value: far below the 4 bits that are held,
+// and below a bf16, FP8 or (for logits) fp16 output.  Centred keys and values
+// measured 98 us where raw ones measured 81 (64 sequences of up to 8192 rows).
 // Centred: c - 8.  A nibble in the low mantissa bits of a power of two is that
 // power plus the nibble, so one subtraction (or one fma for the nibbles that
 // lie 4 bits higher) leaves the number, exactly.
@@ -297,8 +343,7 @@ template <typename TS>
 constexpr int kQueryParts = sizeof(TS) == 4 ? 2 : 1;
 constexpr int kQueryExp = 14;
 // Keys as raw codes: q . c is summed from 0 for every unit, and 8 * sum(q) is
-// taken off in fp32.  fp32 queries use centred codes, whose sums are smaller
-// and so lose less.
+// taken off in fp32.  fp32 queries use centred codes, summed to fp32 rounding.
 template <typename TS>
 constexpr bool kRawKeys = sizeof(TS) != 4;
 // The weights that multiply V: fp16 (2^-11 relative), finer than the rounding
@@ -392,9 +437,10 @@ template <int D>
 constexpr int kUnitBytes = 2 * kBlockBytes<D>;
 template <int D>
 constexpr int kStages = D == 64 ? 3 : 2;
-template <int D, int NT>
+template <int D, int NT, int kParts, int kWarps>
 constexpr int kAttentionSmem = kWarps * (kStages<D> * kUnitBytes<D> + 8 * NT * (D + 4) * 4 +
-                                         8 * NT * 16);
+                                         8 * NT * 16) +
+                               D / 32 * NT * 512 * kParts;
 
 // A weight is held as p * 2^kWeightExp * (scale_v / vref), p relative to a
 // maximum that may lag behind by 2^kLag, so that it is rarely moved: at most
@@ -407,16 +453,70 @@ constexpr float kLeastScale = 7.7037197e-34f;  // 2^-110
 // lanes on a bank: tile row r is the block's row row_of(r).
 __device__ __forceinline__ int row_of(int r) { return (r >> 1) + 4 * (r & 1); }
 
-template <typename TS, int D, int NT, bool kScores>
-__global__ void __launch_bounds__(kThreads, (D == 256 || NT > 1 || sizeof(TS) == 4 ? 2 : 4))
+// Adds to the scores of a head's n cached rows the weights that its query
+// rows' logits give (row j's records start at record `first` * kUnitRows + j),
+// a thread to a row, kBatch rows in flight; ml: each query row's maximum and
+// 1 / sum.
+template <int kThreads>
+__device__ __forceinline__ void add_scores(const AttentionArgs &a, int b, int hk, int n, int rows,
+                                           uint32_t first, const float2 *ml)
+{
+    constexpr int kBatch = 2;
+    const int32_t *table = a.page_table + b * a.table_stride;
+    for (int j0 = threadIdx.x; j0 < n; j0 += kThreads * kBatch) {
+        int64_t at[kBatch];
+        float add[kBatch] = {}, old[kBatch];
+#pragma unroll
+        for (int v = 0; v < kBatch; ++v) {
+            const int j = j0 + v * kThreads;
+            at[v] = -1;
+            if (j < n) {
+                const int64_t page = table[j >> a.pool.log2_page];
+                if (page_ok(a.pool, page))
+                    at[v] = ((page * a.pool.Hk + hk) << a.pool.log2_page) +
+                            (j & ((1 << a.pool.log2_page) - 1));
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < kBatch; ++v) old[v] = at[v] >= 0 ? a.scores[at[v]] : 0.f;
+        const float *x = a.logits + ((int64_t)first * kUnitRows + j0) * a.log_rows;
+        for (int r = 0; r < rows; r += 2) {
+            const bool two = r + 1 < rows;
+            const float2 f = ml[r], f1 = two ? ml[r + 1] : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int v = 0; v < kBatch; ++v) {
+                if (at[v] < 0) continue;
+                const float2 y = *reinterpret_cast<const float2 *>(
+                    x + (int64_t)v * kThreads * a.log_rows + r);
+                add[v] = fmaf(exp2_approx(y.x - f.x), f.y, add[v]);
+                if (two) add[v] = fmaf(exp2_approx(y.y - f1.x), f1.y, add[v]);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < kBatch; ++v)
+            if (at[v] >= 0) a.scores[at[v]] = old[v] + add[v];
+    }
+}
+
+// kWarps: kRunWarps, each block taking its run of the call's units; or more,
+// each block taking one whole item, for calls whose items are few and short
+// enough (see choose_warps): no lengths to add up, no parts to join.
+template <typename TS, int D, int NT>
+constexpr int kRunBlocks = D == 256 || NT > 1 || sizeof(TS) == 4 ? 2 : 4;  // resident on an SM
+template <typename TS, int D, int NT, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, kWarps == kRunWarps ? kRunBlocks<TS, D, NT>
+                                               : kWarps == 8 && kRunBlocks<TS, D, NT> == 4 ? 2 : 1)
 qkn_kv4_attention_kernel(const AttentionArgs a)
 {
     constexpr int kR = 8 * NT;
+    constexpr int kThreads = kWarps * 32;
+    constexpr bool kWhole = kWarps > kRunWarps;
     constexpr int kQP = kQueryParts<TS>;
     constexpr int kWP = kWeightParts<TS>;
     constexpr bool kRawK = kRawKeys<TS>;
     constexpr bool kRawV = kRawValues<TS, NT>;
-    constexpr int kKSteps = D / 16, kMTiles = D / 16;
+    constexpr int kMTiles = D / 16;
+    const bool scored = a.scores != nullptr;
     constexpr int kKWords = D / 32;  // a lane's words of a K row
     constexpr int kVWords = D / 64;  // a lane's words of a V row
     constexpr int kS = kStages<D>;
@@ -424,29 +524,34 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
     constexpr int kChunks = kBB / 16;
 
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int64_t scan[8];
+    __shared__ uint32_t scan[8];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int g = lane / 4, t = lane % 4;
     uint8_t *ring = smem + warp * kS * kUnitBytes<D>;
     float *join = reinterpret_cast<float *>(smem + kWarps * kS * kUnitBytes<D>);
     float4 *join_m = reinterpret_cast<float4 *>(join + kWarps * kR * (D + 4));
+    uint4 *qs = reinterpret_cast<uint4 *>(join_m + kWarps * kR);
+    __shared__ float q_sums[kWarps * kR], q_largest[kWarps];
+    __shared__ float2 row_ml[kR];
     pdl_wait_then_release();
 
     Walk<kR> w;
-    int64_t first = 0;
+    uint32_t first = 0, all = 0;
     int total = 0;
-    if (a.direct) {
+    const int block = (int)(blockIdx.y * gridDim.x + blockIdx.x);
+    if constexpr (kWhole) {
         w.b = blockIdx.x / a.max_items;
         w.item = blockIdx.x - w.b * a.max_items;
         w.unit = 0;
         w.load(a);
         if (w.item >= w.items) return;
         total = w.units - kItemUnits > 0 ? w.units - kItemUnits : 1;
+        first = blockIdx.x * (uint32_t)a.max_units;
     } else {
-        const int64_t all = block_run<kR>(a, scan, w, first, total);
+        all = block_run<kR>(a, scan, w, first, total);
         if (tid == 0) {
-            RunRecord rec = {first, all, total, w.b, w.item, w.unit, -1, 0, 0, 0};
-            a.runs[blockIdx.x] = rec;
+            const RunRecord rec = {first, (uint32_t)max(total, 0), w.b, w.item, w.unit, -1, 0, 0, 0, {}};
+            a.runs[block] = rec;
         }
         if (total <= 0) return;
     }
@@ -468,7 +573,10 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
         head = a.pool.base + (int64_t)(ahead.item % a.pool.Hk) * a.pool.head_bytes + lane * 16;
     };
     if (next < total) {
-        ahead.step(a, warp);
+        if constexpr (kWhole)
+            ahead.unit = warp;
+        else
+            ahead.step(a, warp);
         enter();
         look();
     }
@@ -498,7 +606,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
             next += kWarps;
             if (next < total) {
                 ahead.unit += kWarps;
-                if (ahead.unit >= ahead.units) {
+                if (!kWhole && ahead.unit >= ahead.units) {
                     ahead.step(a, 0);
                     enter();
                 }
@@ -518,68 +626,80 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
         const int hk = w.item % a.pool.Hk, tile = w.item / a.pool.Hk;
         const int rows = min(kR, seq.count * a.group - tile * kR);  // live query rows
         const int seg_units = min(w.units - w.unit, total - at);
-        const bool whole = w.unit == 0 && seg_units >= w.units - kItemUnits;
+        const bool whole = kWhole || (w.unit == 0 && seg_units >= w.units - kItemUnits);
 
-        // The query operand, and what each of the lane's columns needs.
-        uint32_t qf[NT][kQP][kKSteps][2];
+        // The query operand, in shared memory: a 16-byte piece for each lane,
+        // word of a K row, tile and part.  A warp makes every kWarps-th word's;
+        // the largest element and the rows' sums meet in between.
+        constexpr int kMine = (kKWords + kWarps - 1) / kWarps;
+        const float c2 = a.scale * 1.4426950408889634f;
         float qsum[NT][2];
         int vis[NT][2];
         int all_see = seq.n;
-        const float c2 = a.scale * 1.4426950408889634f;
+        float qv[kMine][NT][8];
         float largest = 0.f;
-        const TS *src[NT];
-        bool live[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = nt * 8 + g;
-            live[nt] = r < rows;
-            const int qr = live[nt] ? tile * kR + r : 0;
+            const bool live = r < rows;
+            const int qr = live ? tile * kR + r : 0;
             const int i = qr / a.group;
-            src[nt] = static_cast<const TS *>(a.q) + (int64_t)(seq.start + i) * a.row_stride +
-                      (int64_t)(hk * a.group + qr - i * a.group) * D + t * (D / 4);
-            const int v = live[nt] ? seq.n - seq.count + i + 1 : seq.n;
+            const TS *src = static_cast<const TS *>(a.q) + (int64_t)(seq.start + i) * a.row_stride +
+                            (int64_t)(hk * a.group + qr - i * a.group) * D + t * (D / 4);
+            const int v = live ? seq.n - seq.count + i + 1 : seq.n;
             all_see = min(all_see, v);
 #pragma unroll
             for (int e = 0; e < 2; ++e) vis[nt][e] = __shfl_sync(0xffffffffu, v, (2 * t + e) * 4);
+            float s = 0.f;
 #pragma unroll
-            for (int ww = 0; ww < kKWords; ++ww) {
-                float f[8] = {};
-                if (live[nt]) load8(src[nt] + ww * 8, f);
+            for (int x = 0; x < kMine; ++x) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (fabsf(f[e]) <= 3.402823466e38f) largest = fmaxf(largest, fabsf(f[e]));
+                for (int e = 0; e < 8; ++e) qv[x][nt][e] = 0.f;
+                if (live && warp + x * kWarps < kKWords)
+                    load8(src + (warp + x * kWarps) * 8, qv[x][nt]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s += qv[x][nt][e];
+                    if (fabsf(qv[x][nt][e]) <= 3.402823466e38f)
+                        largest = fmaxf(largest, fabsf(qv[x][nt][e]));
+                }
             }
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            if (t == 0) q_sums[warp * kR + r] = s;
         }
 #pragma unroll
         for (int o = 1; o < 32; o *= 2)
             largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, o));
-        const float factor = power_of_two(min(max(kQueryExp - exponent_of(largest), -103), 113));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float s = 0.f;
-#pragma unroll
-            for (int ww = 0; ww < kKWords; ++ww) {  // again, from L1
-                float f[8] = {};
-                if (live[nt]) load8(src[nt] + ww * 8, f);
-                uint32_t pairs[kQP][4];
-                query_pairs<TS>(f, factor, pairs);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s += f[e];
-#pragma unroll
-                for (int part = 0; part < kQP; ++part)
-#pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        qf[nt][part][ww * 2 + p / 2][p % 2] = pairs[part][p];
-            }
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            s *= c2;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) qsum[nt][e] = __shfl_sync(0xffffffffu, s, (2 * t + e) * 4);
-        }
+        if (lane == 0) q_largest[warp] = largest;
 #pragma unroll
         for (int o = 4; o < 32; o *= 2)
             all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, o));
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) largest = fmaxf(largest, q_largest[i]);
+        const float factor = power_of_two(min(max(kQueryExp - exponent_of(largest), -103), 113));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int x = 0; x < kMine; ++x)
+                if (warp + x * kWarps < kKWords) {
+                    uint32_t pairs[kQP][4];
+                    query_pairs<TS>(qv[x][nt], factor, pairs);
+#pragma unroll
+                    for (int part = 0; part < kQP; ++part)
+                        qs[(((warp + x * kWarps) * NT + nt) * kQP + part) * 32 + lane] = make_uint4(
+                            pairs[part][0], pairs[part][1], pairs[part][2], pairs[part][3]);
+                }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float s = 0.f;
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) s += q_sums[i * kR + nt * 8 + 2 * t + e];
+                qsum[nt][e] = s * c2;
+            }
+        }
+        __syncthreads();
         // What the product of the operands has to be multiplied by.
         const float c_s = c2 * power_of_two((kRawK ? 24 : 0) - exponent_of(factor));
 
@@ -594,47 +714,51 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
             const uint8_t *unit = ring + stage * kUnitBytes<D>;
             const int base = (w.unit + k) * kUnitRows;
 
-            float s[2][NT][4];
+            float s[2][NT][4] = {};
+            uint32_t kw[2][2][kKWords];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint8_t *blk = unit + half * kBB;
-                uint32_t kw[2][kKWords];
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint8_t *p = blk + (row_of(g) + 8 * r) * (D / 2) + t * (D / 8);
+                    const uint8_t *p =
+                        unit + half * kBB + (row_of(g) + 8 * r) * (D / 2) + t * (D / 8);
                     if constexpr (kKWords == 2) {
                         const uint2 u = *reinterpret_cast<const uint2 *>(p);
-                        kw[r][0] = u.x;
-                        kw[r][1] = u.y;
+                        kw[half][r][0] = u.x;
+                        kw[half][r][1] = u.y;
                     } else {
 #pragma unroll
                         for (int v = 0; v < kKWords / 4; ++v) {
                             const uint4 u = *(reinterpret_cast<const uint4 *>(p) + v);
-                            kw[r][4 * v] = u.x;
-                            kw[r][4 * v + 1] = u.y;
-                            kw[r][4 * v + 2] = u.z;
-                            kw[r][4 * v + 3] = u.w;
+                            kw[half][r][4 * v] = u.x;
+                            kw[half][r][4 * v + 1] = u.y;
+                            kw[half][r][4 * v + 2] = u.z;
+                            kw[half][r][4 * v + 3] = u.w;
                         }
                     }
                 }
 #pragma unroll
+            for (int ww = 0; ww < kKWords; ++ww) {
+                uint4 q[NT][kQP];
+#pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[half][nt][e] = 0.f;
+                    for (int part = 0; part < kQP; ++part)
+                        q[nt][part] = qs[((ww * NT + nt) * kQP + part) * 32 + lane];
 #pragma unroll
-                for (int ww = 0; ww < kKWords; ++ww) {
+                for (int half = 0; half < 2; ++half) {
                     uint32_t lo[4], hi[4];
-                    unpack_nibbles<kRawK>(kw[0][ww], lo);
-                    unpack_nibbles<kRawK>(kw[1][ww], hi);
+                    unpack_nibbles<kRawK>(kw[half][0][ww], lo);
+                    unpack_nibbles<kRawK>(kw[half][1][ww], hi);
 #pragma unroll
-                    for (int st = 0; st < 2; ++st)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int part = 0; part < kQP; ++part)
-                                mma(s[half][nt], lo[2 * st], hi[2 * st], lo[2 * st + 1],
-                                    hi[2 * st + 1], qf[nt][part][ww * 2 + st][0],
-                                    qf[nt][part][ww * 2 + st][1]);
+                        for (int part = 0; part < kQP; ++part) {
+                            mma(s[half][nt], lo[0], hi[0], lo[1], hi[1], q[nt][part].x,
+                                q[nt][part].y);
+                            mma(s[half][nt], lo[2], hi[2], lo[3], hi[3], q[nt][part].z,
+                                q[nt][part].w);
+                        }
                 }
             }
 
@@ -690,8 +814,8 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
                             top[nt][e] = fmaxf(top[nt][e], s[half][nt][2 * r + e]);
-                    if constexpr (kScores) {
-                        float *to = a.logits + ((first + at + k) * kUnitRows + half * kBlockRows +
+                    if (scored) {
+                        float *to = a.logits + ((int64_t)(first + at + k) * kUnitRows + half * kBlockRows +
                                                 row_of(g) + 8 * r) * a.log_rows;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -900,23 +1024,20 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
         }
         __syncthreads();
         // Eight elements of a row to a thread; the warps are added in order.
-        const int slot = 2 * blockIdx.x + (seg_index > 0 ? 1 : 0);
+        const int slot = 2 * block + (seg_index > 0 ? 1 : 0);
         for (int i = tid; i < rows * (D / 8); i += kThreads) {
             const int r = i / (D / 8), d = (i % (D / 8)) * 8;
-            float4 mlz[kWarps];
             float mm = -INFINITY, ll = 0.f, zz = 0.f;
 #pragma unroll
-            for (int v = 0; v < kWarps; ++v) {
-                mlz[v] = join_m[v * kR + r];
-                mm = fmaxf(mm, mlz[v].x);
-            }
+            for (int v = 0; v < kWarps; ++v) mm = fmaxf(mm, join_m[v * kR + r].x);
             float o[8] = {};
-#pragma unroll
+#pragma unroll 4
             for (int v = 0; v < kWarps; ++v) {
-                const float e = mm == -INFINITY ? 0.f : exp2_approx(mlz[v].x - mm);
-                ll = fmaf(mlz[v].y, e, ll);
-                zz = fmaf(mlz[v].z, e, zz);
-                const float ev = e * mlz[v].w;
+                const float4 mlz = join_m[v * kR + r];
+                const float e = mm == -INFINITY ? 0.f : exp2_approx(mlz.x - mm);
+                ll = fmaf(mlz.y, e, ll);
+                zz = fmaf(mlz.z, e, zz);
+                const float ev = e * mlz.w;
                 float x[8];
                 load8(join + (v * kR + r) * (D + 4) + d, x);
 #pragma unroll
@@ -937,9 +1058,11 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                     if (a.lse != nullptr)
                         a.lse[(int64_t)(seq.start + qi) * a.Hq + h] =
                             ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
-                    if constexpr (kScores)
-                        a.row_ml[(int64_t)w.b * a.max_q * a.Hq + qi * a.Hq + h] =
-                            make_float2(ll == 0.f ? 0.f : mm, inv);
+                    const float2 ml = make_float2(ll == 0.f ? 0.f : mm, inv);
+                    if constexpr (kWhole)
+                        row_ml[r] = ml;
+                    else if (scored)
+                        a.row_ml[(int64_t)w.b * a.max_q * a.Hq + qi * a.Hq + h] = ml;
                 }
             } else {
                 float *to = a.part + ((int64_t)slot * kR + r) * D + d;
@@ -947,15 +1070,21 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                 if (d == 0) a.part_ml[(int64_t)slot * kR + r] = make_float2(mm, ll);
             }
         }
+        if constexpr (kWhole) {
+            // The item's rows' weights, from the logits that this block wrote.
+            if (scored) {
+                __syncthreads();
+                add_scores<kThreads>(a, w.b, hk, seq.n, rows, first, row_ml);
+            }
+            return;
+        }
         if (tid == 0 && w.unit == 0 && !whole) {
             // The item goes on in the blocks behind this one.
-            RunRecord &rec = a.runs[blockIdx.x];
-            const int64_t all = rec.all, blocks = all < gridDim.x ? all : gridDim.x;
-            const int64_t last_unit = first + at + w.units - kItemUnits - 1;
+            RunRecord &rec = a.runs[block];
             rec.join_b = w.b;
             rec.join_item = w.item;
             rec.join_slot = slot;
-            rec.join_last = (int)(((last_unit + 1) * blocks - 1) / all);
+            rec.join_last = (int)Runs(all).holder(a, first + at + w.units - kItemUnits - 1);
         }
         __syncthreads();
         at += seg_units;
@@ -972,7 +1101,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
 // part of the same rows.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 2;
-template <typename TS, int D, int kR, bool kScores>
+template <typename TS, int D, int kR>
 __global__ void __launch_bounds__(kJoinThreads) qkn_kv4_join_kernel(const AttentionArgs a)
 {
     constexpr int kLanes = kJoinRows * D / 4;
@@ -1048,7 +1177,7 @@ __global__ void __launch_bounds__(kJoinThreads) qkn_kv4_join_kernel(const Attent
         if (a.lse != nullptr)
             a.lse[(int64_t)(seq.start + qi) * a.Hq + h] =
                 none ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
-        if constexpr (kScores)
+        if (a.scores != nullptr)
             a.row_ml[(int64_t)rec.join_b * a.max_q * a.Hq + qi * a.Hq + h] =
                 make_float2(none ? 0.f : mm, inv);
     }
@@ -1072,11 +1201,12 @@ __global__ void __launch_bounds__(kScoreThreads) qkn_kv4_scores_kernel(const Att
     w.b = rec.b;
     w.item = rec.item;
     w.unit = rec.unit;
-    if (rec.total > 0) w.load(a);
+    const int total = (int)rec.total;
+    if (total > 0) w.load(a);
     // Batches of the run, item by item; every kStep-th is this warp's.
     int k = 0, batch = 0;
-    while (k < rec.total) {
-        const int left = min(w.units - w.unit, rec.total - k);
+    while (k < total) {
+        const int left = min(w.units - w.unit, total - k);
         const int live = min(w.units - kItemUnits - w.unit, left);
         const int batches = (live + kBatch - 1) / kBatch;
         // Only a head's first tile stands for its units.
@@ -1092,7 +1222,8 @@ __global__ void __launch_bounds__(kScoreThreads) qkn_kv4_scores_kernel(const Att
                 const int u = i * kBatch;
                 int64_t at[kBatch];
                 float add[kBatch] = {}, old[kBatch];
-                const float *x = a.logits + ((rec.first + k + u) * kUnitRows + lane) * a.log_rows;
+                const float *x =
+                    a.logits + ((int64_t)(rec.first + k + u) * kUnitRows + lane) * a.log_rows;
 #pragma unroll
                 for (int v = 0; v < kBatch; ++v) {
                     const int j = (w.unit + u + v) * kUnitRows + lane;
@@ -1131,7 +1262,7 @@ __global__ void __launch_bounds__(kScoreThreads) qkn_kv4_scores_kernel(const Att
             batch += batches;
         }
         k += left;
-        if (k < rec.total) w.step(a, left);
+        if (k < total) w.step(a, left);
     }
 }
 

@@ -213,9 +213,15 @@ struct Read {
 };
 
 // -------------------------------------------------------------- attention --
+// Items go to one block each where they have at most 8 units to each of 16
+// warps or 4 to each of 8, in one wave, or kShortUnits in two.  (128 heads of
+// 500 to 2500 rows, D = 128: 14.7 us, and 20.7 split; 28 heads of 1 to 2049
+// rows, D = 256 in fp32, 8 warps: 36 us, and 24 split.)
+constexpr int kShortUnits = 16;
 constexpr int kMaxBlocks = 1024;  // of the attention kernel (four to an SM at most)
-// Items of at most this many units are not split: one launch instead of two.
-constexpr int64_t kDirectUnits = 16;
+// Where the rows of its blocks begin in the units, in 128ths, by resident
+// blocks to an SM (see Runs).
+constexpr int kZones[4][4] = {{0, 0, 0, 0}, {0, 64, 0, 0}, {0, 43, 86, 0}, {0, 32, 64, 96}};
 
 // Query tiles (of 8 columns) of an item: as many as the rows of a key/value
 // head fill, as the register budget allows (the query operand and the sums of
@@ -230,7 +236,7 @@ int query_tiles(int dtype, int D, int64_t rows)
 
 struct AttentionPlan {
     int nt, log_rows, max_items;
-    bool direct;
+    bool whole;  // items may go to one block each
     int64_t max_units;  // of an item
     int64_t runs, part, part_ml, row_ml, logits, bytes;  // offsets in the workspace, and its size
 };
@@ -245,7 +251,7 @@ AttentionPlan attention_plan(int64_t B, int dtype, int Hq, int Hk, int D, int ma
     const int64_t tiles = (rows + kr - 1) / kr;
     p.max_units = (max_kv + kUnitRows - 1) / kUnitRows + kItemUnits;
     p.max_items = (int)(tiles * Hk);
-    p.direct = !scores && p.max_units - kItemUnits <= kDirectUnits && B * tiles * Hk <= INT32_MAX;
+    p.whole = (!scores || tiles == 1) && B * tiles * Hk <= INT32_MAX;
     p.log_rows = (int)(rows < kr ? (rows + 1) / 2 * 2 : kr);
     // Sizes may pass 63 bits for arguments that no buffer could have.
     __int128 at = 0;
@@ -265,28 +271,58 @@ AttentionPlan attention_plan(int64_t B, int dtype, int Hq, int Hk, int D, int ma
     return p;
 }
 
-template <typename TS, int D, int NT, bool kScores>
-int launch_attention(const AttentionArgs &a, const AttentionPlan &p, cudaStream_t stream)
+template <typename TS, int D, int NT, int kWarps>
+int launch_whole(const AttentionArgs &a, const AttentionPlan &p, int sms, cudaStream_t stream,
+                 bool *done)
 {
     static std::atomic<int> cache[kMaxDevices];
-    constexpr int smem = kAttentionSmem<D, NT>;
-    auto kern = qkn_kv4_attention_kernel<TS, D, NT, kScores>;
+    constexpr int smem = kAttentionSmem<D, NT, kQueryParts<TS>, kWarps>;
+    auto kern = qkn_kv4_attention_kernel<TS, D, NT, kWarps>;
+    int per_sm = 0, rc;
+    if ((rc = blocks_per_sm(kern, kWarps * 32, smem, cache, &per_sm)) != QKN_OK) return rc;
+    const int64_t items = a.B * (int64_t)p.max_items, room = (int64_t)sms * per_sm;
+    const int64_t most = p.max_units - kItemUnits;
+    *done = (items <= room && most <= kWarps * kWarps / 2) ||
+            (items <= 2 * room && most <= kShortUnits);
+    if (!*done) return QKN_OK;
+    return launch(kern, dim3((unsigned)items), kWarps * 32, smem, stream, a);
+}
+
+template <typename TS, int D, int NT>
+int launch_attention(const AttentionArgs &a, const AttentionPlan &p, cudaStream_t stream)
+{
     int per_sm = 0, sms = 0, rc;
     if ((rc = device_sms(&sms)) != QKN_OK) return rc;
-    if ((rc = blocks_per_sm(kern, kThreads, smem, cache, &per_sm)) != QKN_OK) return rc;
-    if (p.direct)
-        return launch(kern, dim3((unsigned)(a.B * (int64_t)p.max_items)), kThreads, smem, stream, a);
+    if (p.whole) {
+        // The most warps that the registers (and shared memory) of an SM hold.
+        bool done = false;
+        if constexpr (kRunBlocks<TS, D, NT> == 4)
+            if ((rc = launch_whole<TS, D, NT, 16>(a, p, sms, stream, &done)) != QKN_OK || done)
+                return rc;
+        if constexpr (D < 256 || NT == 1)
+            if ((rc = launch_whole<TS, D, NT, 8>(a, p, sms, stream, &done)) != QKN_OK || done)
+                return rc;
+    }
+    static std::atomic<int> cache[kMaxDevices];
+    constexpr int smem = kAttentionSmem<D, NT, kQueryParts<TS>, kRunWarps>;
+    auto kern = qkn_kv4_attention_kernel<TS, D, NT, kRunWarps>;
+    if ((rc = blocks_per_sm(kern, kRunThreads, smem, cache, &per_sm)) != QKN_OK) return rc;
     const int64_t units = (int64_t)a.B * p.max_items * p.max_units;
-    int64_t grid = (int64_t)sms * per_sm;
-    if (grid > kMaxBlocks) grid = kMaxBlocks;
-    if (grid > units) grid = units;
-    const dim3 blocks((unsigned)grid);
-    if ((rc = launch(kern, blocks, kThreads, smem, stream, a)) != QKN_OK) return rc;
-    rc = launch(qkn_kv4_join_kernel<TS, D, 8 * NT, kScores>,
-                dim3((unsigned)grid, 8 * NT / kJoinRows), kJoinThreads, 0, stream, a);
-    if (rc != QKN_OK || !kScores) return rc;
-    return launch(qkn_kv4_scores_kernel<8 * NT>, dim3((unsigned)grid, kScoreSplit), kScoreThreads,
-                  0, stream, a);
+    if (per_sm > 4) per_sm = 4;
+    if ((int64_t)sms * per_sm > kMaxBlocks) return QKN_ERR_UNSUPPORTED;
+    // Whole rows of blocks, one on every SM; fewer blocks where the call cannot
+    // have a unit for each.
+    dim3 shape((unsigned)sms, (unsigned)per_sm);
+    if (units < (int64_t)sms * per_sm) shape = dim3((unsigned)units, 1u);
+    AttentionArgs args = a;
+    for (int y = 0; y < 4; ++y) args.zones[y] = kZones[per_sm - 1][y];
+    const unsigned blocks = shape.x * shape.y;
+    if ((rc = launch(kern, shape, kRunThreads, smem, stream, args)) != QKN_OK) return rc;
+    rc = launch(qkn_kv4_join_kernel<TS, D, 8 * NT>, dim3(blocks, 8 * NT / kJoinRows), kJoinThreads,
+                0, stream, args);
+    if (rc != QKN_OK || a.scores == nullptr) return rc;
+    return launch(qkn_kv4_scores_kernel<8 * NT>, dim3(blocks, kScoreSplit), kScoreThreads, 0, stream,
+                  args);
 }
 
 struct Attention {
@@ -297,8 +333,7 @@ struct Attention {
 #define QKN_KV4_NT(NT)                                                                         \
     if constexpr (NT == 1 || NT * kTile <= 192)                                                \
         if (p.nt == NT)                                                                        \
-            return a.scores != nullptr ? launch_attention<TS, D, NT, true>(a, p, stream)       \
-                                       : launch_attention<TS, D, NT, false>(a, p, stream);
+            return launch_attention<TS, D, NT>(a, p, stream);
         QKN_KV4_NT(1)
         QKN_KV4_NT(2)
         QKN_KV4_NT(4)
@@ -466,6 +501,8 @@ int qknorm_kv4_attention(const void *q, int dtype, int64_t T, int Hq, int Hk, in
     const AttentionPlan plan =
         attention_plan(B, dtype, Hq, Hk, D, max_q, max_pages * page_size, scores != nullptr);
     if (workspace_bytes < plan.bytes) return QKN_ERR_SHAPE;
+    if ((__int128)B * plan.max_items * plan.max_units > INT32_MAX)
+        return QKN_ERR_SHAPE;
     AttentionArgs a = {};
     a.q = q;
     a.T = T;
@@ -485,7 +522,7 @@ int qknorm_kv4_attention(const void *q, int dtype, int64_t T, int Hq, int Hk, in
     a.out = out;
     a.lse = lse;
     a.scores = scores;
-    a.direct = plan.direct;
+    a.max_units = (int)plan.max_units;
     a.max_items = plan.max_items;
     a.log_rows = plan.log_rows;
     uint8_t *ws = static_cast<uint8_t *>(workspace);

@@ -105,11 +105,12 @@ int qknorm_kv4_read(const void *pool, int64_t num_pages, int page_size, int Hk, 
  * one call: their additions would race.)
  *
  * Arithmetic: q is taken in fp16 relative to the largest element of its group
- * (which loses nothing of bf16, fp16 and FP8 that an fp32 sum would keep; fp32
- * is held in two fp16 parts; magnitudes up to 1e35), its products with the
- * whole codes are exact, and softmax statistics and all sums are fp32.  The
- * weights that multiply V are rounded to fp16 (bf16 and FP8 outputs), or held
- * in two fp16 parts (fp16 and fp32 outputs).
+ * (which loses nothing of bf16, fp16 and FP8 that the sums would keep; fp32 is
+ * held in two fp16 parts; magnitudes up to 1e35).  Softmax statistics and all
+ * sums are fp32.  q . K is good to D/16 * 2^-13 * max|q| * scale_k (fp32
+ * queries: to fp32 rounding).  The weights that multiply V are rounded to fp16,
+ * and V's sums are good to 2^-13 of scale_v (bf16 and FP8 outputs), or held in
+ * two fp16 parts and summed to fp32 rounding (fp16 and fp32 outputs).
  *
  * workspace: device memory, 16-byte aligned, of at least the bytes that
  * qknorm_kv4_attention_workspace gives for the same B, heads, D, dtype, max_q,

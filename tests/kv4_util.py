@@ -64,13 +64,17 @@ class Held:
 
 
 def attend(cache, q, Hq, table, lens, starts, scale, dtype):
-    """out, lse, the weights added to each row, and an error bound for out.
+    """out, lse, the weights added to each row, and error bounds.
 
     The bound for out counts: one rounding of the output; the weights that
     multiply V, rounded to fp16 (2^-11 relative, at least 2^-25 of the largest
-    weight times V scale) or held in two fp16 parts (2^-21); and the relative error of
-    each weight, exp(d) - 1 with d the fp32 error of a logit: D + 16 roundings
-    of 2^-23 each (the matrix unit may truncate) of the sum of |terms|."""
+    weight times V scale) or held in two fp16 parts (2^-21); and the relative
+    error of each weight, exp(d) - 1 with d the error of a logit: D + 16
+    roundings of 2^-23 each (the matrix unit may truncate) of the sum of |terms|.
+    Codes that enter a product as fp16 subnormal numbers (c * 2^-24, exponent
+    field 2^-14; all types but fp32, and V for bf16 and FP8 only) are aligned by
+    that field, so a product of 16 terms keeps 2^-23 of the largest other
+    operand x 2^-14, which is 2^-13 of that operand in steps of the code."""
     T, Hk, D, page = q.shape[0], cache.Hk, cache.D, cache.page_size
     G = Hq // Hk
     held = Held(cache)
@@ -100,6 +104,9 @@ def attend(cache, q, Hq, table, lens, starts, scale, dtype):
             terms = np.einsum("hgd,hnd->hgn", np.abs(x[t]),
                               np.abs(ck[:, s]) * sk[:, s, None] + np.abs(mk[:, s, None])) * abs(scale)
             d = (D + 16) * 2.0 ** -23 * terms + 2.0 ** -22 * (1 + np.abs(w).max())
+            if dtype != "fp32":
+                d += D / 16 * 2.0 ** -13 * np.abs(x[t]).max((1, 2))[:, None, None] * (
+                    sk[:, None, s] * abs(scale))
             top = w.max(-1, keepdims=True)
             e = np.exp(w - top)
             total = e.sum(-1, keepdims=True)
@@ -117,7 +124,8 @@ def attend(cache, q, Hq, table, lens, starts, scale, dtype):
             # and each addition rounds (or truncates) at 2^-23 of that.
             eights = 8 * np.einsum("hgn,hn->hg", p, sv[:, s])[..., None]
             bound[t] = (part * mag + least + rel * (mag + mids)
-                        + (sees + 16) * 2.0 ** -23 * (mag + eights + mids))
+                        + (sees + 16) * 2.0 ** -23 * (mag + eights + mids)
+                        + (2.0 ** -13 / 8 * eights if part == 2.0 ** -11 else 0.0))
             j = np.arange(sees)
             at = np.asarray(pages)[j // page]
             add[at, :, j % page] += p.sum(1).T
