@@ -9,6 +9,8 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,10 +19,10 @@ CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, "qknorm.cu")]
 HEADERS = [os.path.join(INCLUDE, "qknorm.h")] + sorted(
     os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh"))
-# The 4-bit key/value cache (include/qknorm_kv4.h): a translation unit of its
-# own in the same library.
+# The 4-bit key/value cache (include/qknorm_kv4.h): translation units of their
+# own in the same library, compiled side by side.
 KV4_CSRC = os.path.join(CSRC, "kv4")
-KV4_SOURCES = [os.path.join(KV4_CSRC, "kv4.cu")]
+KV4_SOURCES = sorted(os.path.join(KV4_CSRC, f) for f in os.listdir(KV4_CSRC) if f.endswith(".cu"))
 KV4_HEADERS = [os.path.join(INCLUDE, "qknorm_kv4.h")] + sorted(
     os.path.join(KV4_CSRC, f) for f in os.listdir(KV4_CSRC) if f.endswith(".cuh"))
 LIB_PATH = os.path.join(PKG, "libqknorm.so")
@@ -102,9 +104,18 @@ def build(force: bool = False, extra_flags=(), out: str = LIB_PATH) -> str:
     if not force and out == LIB_PATH and not is_stale():
         return out
     tmp = out + ".%d.tmp" % os.getpid()
-    cmd = [nvcc(), *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, *SOURCES, *KV4_SOURCES, "-t", "2",
-           "-o", tmp]
-    subprocess.check_call(cmd)
+    flags = [nvcc(), *NVCC_FLAGS, *extra_flags]
+    compile_flags = [f for f in flags if f not in ("-shared", "-cudart", "static")]
+    sources = SOURCES + KV4_SOURCES
+    with tempfile.TemporaryDirectory(prefix="qknorm_build_") as d:
+        objects = [os.path.join(d, "%d.o" % i) for i in range(len(sources))]
+
+        def compile_one(pair):
+            subprocess.check_call([*compile_flags, "-I", INCLUDE, "-c", pair[0], "-o", pair[1]])
+
+        with ThreadPoolExecutor() as pool:
+            list(pool.map(compile_one, zip(sources, objects)))
+        subprocess.check_call([*flags, *objects, "-o", tmp])
     os.replace(tmp, out)
     return out
 

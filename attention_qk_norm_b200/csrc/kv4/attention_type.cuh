@@ -1,0 +1,108 @@
+// attention_type.cuh -- the attention kernels of one storage type and their
+// launches; each attention_*.cu defines QKN_KV4_TYPE and QKN_KV4_NAME and
+// includes this, so that the types compile side by side.
+// Part of libqknorm.so.
+#include "host.cuh"
+
+QKN_KV4_TYPES(QKN_KV4_DECLARE)
+
+namespace {
+
+// Items go to one block each where they have at most 8 units to each of 16
+// warps or 4 to each of 8, in one wave, or kShortUnits in two.  (128 heads of
+// 500 to 2500 rows, D = 128: 14.7 us, and 20.7 split; 28 heads of 1 to 2049
+// rows, D = 256 in fp32, 8 warps: 36 us, and 24 split.)
+constexpr int kShortUnits = 16;
+// Where the rows of its blocks begin in the units, in 128ths, by resident
+// blocks to an SM (see Runs).
+constexpr int kZones[4][4] = {{0, 0, 0, 0}, {0, 64, 0, 0}, {0, 43, 86, 0}, {0, 32, 64, 96}};
+
+template <typename TS, int D, int NT, int kWarps>
+int launch_whole(const AttentionArgs &a, const AttentionPlan &p, int sms, cudaStream_t stream,
+                 bool *done)
+{
+    static std::atomic<int> cache[kMaxDevices];
+    constexpr int smem = kAttentionSmem<D, NT, kQueryParts<TS>, kWarps>;
+    auto kern = qkn_kv4_attention_kernel<TS, D, NT, kWarps>;
+    int per_sm = 0, rc;
+    if ((rc = blocks_per_sm(kern, kWarps * 32, smem, cache, &per_sm)) != QKN_OK) return rc;
+    const int64_t items = a.B * (int64_t)p.max_items, room = (int64_t)sms * per_sm;
+    const int64_t most = p.max_units - kItemUnits;
+    *done = (items <= room && most <= kWarps * kWarps / 2) ||
+            (items <= 2 * room && most <= kShortUnits);
+    if (!*done) return QKN_OK;
+    return launch(kern, dim3((unsigned)items), kWarps * 32, smem, stream, a);
+}
+
+template <typename TS, int D, int NT>
+int launch_attention(const AttentionArgs &a, const AttentionPlan &p, cudaStream_t stream)
+{
+    int per_sm = 0, sms = 0, rc;
+    if ((rc = device_sms(&sms)) != QKN_OK) return rc;
+    if (p.whole) {
+        // The most warps that the registers (and shared memory) of an SM hold.
+        bool done = false;
+        if constexpr (kRunBlocks<TS, D, NT> == 4)
+            if ((rc = launch_whole<TS, D, NT, 16>(a, p, sms, stream, &done)) != QKN_OK || done)
+                return rc;
+        if constexpr (D < 256 || NT == 1)
+            if ((rc = launch_whole<TS, D, NT, 8>(a, p, sms, stream, &done)) != QKN_OK || done)
+                return rc;
+    }
+    static std::atomic<int> cache[kMaxDevices];
+    constexpr int smem = kAttentionSmem<D, NT, kQueryParts<TS>, kRunWarps>;
+    auto kern = qkn_kv4_attention_kernel<TS, D, NT, kRunWarps>;
+    if ((rc = blocks_per_sm(kern, kRunThreads, smem, cache, &per_sm)) != QKN_OK) return rc;
+    const int64_t units = (int64_t)a.B * p.max_items * p.max_units;
+    if (per_sm > 4) per_sm = 4;
+    if ((int64_t)sms * per_sm > kMaxBlocks) return QKN_ERR_UNSUPPORTED;
+    // Whole rows of blocks, one on every SM; fewer blocks where the call cannot
+    // have a unit for each.
+    dim3 shape((unsigned)sms, (unsigned)per_sm);
+    if (units < (int64_t)sms * per_sm) shape = dim3((unsigned)units, 1u);
+    AttentionArgs args = a;
+    for (int y = 0; y < 4; ++y) args.zones[y] = kZones[per_sm - 1][y];
+    const unsigned blocks = shape.x * shape.y;
+    if ((rc = launch(kern, shape, kRunThreads, smem, stream, args)) != QKN_OK) return rc;
+    rc = launch(qkn_kv4_join_kernel<TS, D, 8 * NT>, dim3(blocks, 8 * NT / kJoinRows), kJoinThreads,
+                0, stream, args);
+    if (rc != QKN_OK || a.scores == nullptr) return rc;
+    return launch(qkn_kv4_scores_kernel<8 * NT>, dim3(blocks, kScoreSplit), kScoreThreads, 0, stream,
+                  args);
+}
+
+template <int D>
+int run_attention(const AttentionArgs &a, const AttentionPlan &p, cudaStream_t stream)
+{
+    using TS = QKN_KV4_TYPE;
+    constexpr int kTile = D / 16 * (2 * kQueryParts<TS> + 4);
+    if (p.nt == 1) return launch_attention<TS, D, 1>(a, p, stream);
+    if constexpr (2 * kTile <= 192)
+        if (p.nt == 2) return launch_attention<TS, D, 2>(a, p, stream);
+    if constexpr (4 * kTile <= 192)
+        if (p.nt == 4) return launch_attention<TS, D, 4>(a, p, stream);
+    return QKN_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+#define QKN_KV4_JOIN2(A, B) A##B
+#define QKN_KV4_JOIN(A, B) QKN_KV4_JOIN2(A, B)
+
+int QKN_KV4_JOIN(qkn_kv4_attention_, QKN_KV4_NAME)(int D, const void *args, const void *plan,
+                                                   cudaStream_t stream)
+{
+    const AttentionArgs &a = *static_cast<const AttentionArgs *>(args);
+    const AttentionPlan &p = *static_cast<const AttentionPlan *>(plan);
+    switch (D) {
+    case 64: return run_attention<64>(a, p, stream);
+    case 128: return run_attention<128>(a, p, stream);
+    default: return run_attention<256>(a, p, stream);
+    }
+}
+
+int QKN_KV4_JOIN(qkn_kv4_bad_pages_, QKN_KV4_NAME)(unsigned int *count)
+{
+    const cudaError_t e = cudaMemcpyFromSymbol(count, g_kv4_bad_pages, sizeof(unsigned int));
+    return e == cudaSuccess ? QKN_OK : cuda_fail(e);
+}

@@ -1,0 +1,109 @@
+// host.cuh -- host-side helpers of the 4-bit cache's translation units: errors,
+// device sizes, launches, and the plan of an attention call.
+// Part of libqknorm.so.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "qknorm_kv4.h"
+
+#include "attention.cuh"
+
+// The calling thread's last CUDA error here (kv4.cu).
+__attribute__((visibility("hidden"))) void qkn_kv4_set_error(int e);
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+int cuda_fail(cudaError_t e)
+{
+    qkn_kv4_set_error((int)e);
+    return QKN_ERR_CUDA;
+}
+
+// SMs of the current device, looked up once for each.
+std::atomic<int> g_sms[kMaxDevices];
+
+int device_sms(int *sms)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 0 || dev >= kMaxDevices) return QKN_ERR_UNSUPPORTED;
+    int n = g_sms[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return cuda_fail(e);
+        g_sms[dev].store(n, std::memory_order_relaxed);
+    }
+    *sms = n;
+    return QKN_OK;
+}
+
+template <typename... Params, typename... Args>
+int launch(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+           Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? QKN_OK : cuda_fail(e);
+}
+
+// Resident blocks of a kernel on an SM, looked up once for each device with
+// its shared-memory limit raised.
+template <typename Kern>
+int blocks_per_sm(Kern kern, int threads, int smem, std::atomic<int> *cache, int *out)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 0 || dev >= kMaxDevices) return QKN_ERR_UNSUPPORTED;
+    int n = cache[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+        if (smem > 0)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (n < 1) return QKN_ERR_UNSUPPORTED;
+        cache[dev].store(n, std::memory_order_release);
+    }
+    *out = n;
+    return QKN_OK;
+}
+
+constexpr int kMaxBlocks = 1024;  // of the attention kernel (four to an SM at most)
+
+struct AttentionPlan {
+    int nt, log_rows, max_items;
+    bool whole;  // items may go to one block each
+    int64_t max_units;  // of an item
+    int64_t runs, part, part_ml, row_ml, logits, bytes;  // offsets in the workspace, and its size
+};
+
+}  // namespace
+
+// The attention of each storage type, in a translation unit of its own, and
+// that unit's counter of bad pages.
+#define QKN_KV4_TYPES(F) F(bf16) F(fp16) F(fp32) F(e4m3)
+#define QKN_KV4_DECLARE(NAME)                                                                  \
+    extern "C" __attribute__((visibility("hidden"))) int qkn_kv4_attention_##NAME(             \
+        int D, const void *args, const void *plan, cudaStream_t stream);                       \
+    extern "C" __attribute__((visibility("hidden"))) int qkn_kv4_bad_pages_##NAME(             \
+        unsigned int *count);

@@ -1,68 +1,22 @@
 // kv4.cu -- the 4-bit key/value cache (declared in include/qknorm_kv4.h):
-// argument checks, launch shapes and the C entry points.  The library's second
-// translation unit; the kernels are in the headers beside it.
-#include <cuda_runtime.h>
-
-#include <math.h>
-#include <stdint.h>
-
-#include <atomic>
-
-#include "qknorm_kv4.h"
-
-#include "attention.cuh"
+// argument checks, launch shapes and the C entry points.  The kernels are in the
+// headers beside it; the attention kernels compile in attention_*.cu, one for
+// each storage type.
 #include "cache.cuh"
 #include "evict.cuh"
+#include "host.cuh"
+
+QKN_KV4_TYPES(QKN_KV4_DECLARE)
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-
 thread_local int g_last_error = 0;
 
-int cuda_fail(cudaError_t e)
-{
-    g_last_error = (int)e;
-    return QKN_ERR_CUDA;
-}
+}  // namespace
 
-// SMs of the current device, looked up once for each.
-std::atomic<int> g_sms[kMaxDevices];
+void qkn_kv4_set_error(int e) { g_last_error = e; }
 
-int device_sms(int *sms)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (dev < 0 || dev >= kMaxDevices) return QKN_ERR_UNSUPPORTED;
-    int n = g_sms[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return cuda_fail(e);
-        g_sms[dev].store(n, std::memory_order_relaxed);
-    }
-    *sms = n;
-    return QKN_OK;
-}
-
-template <typename... Params, typename... Args>
-int launch(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
-           Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    return e == cudaSuccess ? QKN_OK : cuda_fail(e);
-}
+namespace {
 
 bool aligned(const void *p, unsigned bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
 
@@ -142,29 +96,6 @@ int stream_grid(uint64_t groups, int lanes, int per_sm, unsigned *grid)
     return QKN_OK;
 }
 
-// Resident blocks of a kernel on an SM, looked up once for each device with
-// its shared-memory limit raised.
-template <typename Kern>
-int blocks_per_sm(Kern kern, int threads, int smem, std::atomic<int> *cache, int *out)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (dev < 0 || dev >= kMaxDevices) return QKN_ERR_UNSUPPORTED;
-    int n = cache[dev].load(std::memory_order_acquire);
-    if (n == 0) {
-        if (smem > 0)
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem);
-        if (e != cudaSuccess) return cuda_fail(e);
-        if (n < 1) return QKN_ERR_UNSUPPORTED;
-        cache[dev].store(n, std::memory_order_release);
-    }
-    *out = n;
-    return QKN_OK;
-}
-
 struct Append {
     template <typename TS, int D>
     static int run(void *qkv, int64_t T, int Hq, int Hk, int64_t row_stride, const float *gq,
@@ -213,16 +144,6 @@ struct Read {
 };
 
 // -------------------------------------------------------------- attention --
-// Items go to one block each where they have at most 8 units to each of 16
-// warps or 4 to each of 8, in one wave, or kShortUnits in two.  (128 heads of
-// 500 to 2500 rows, D = 128: 14.7 us, and 20.7 split; 28 heads of 1 to 2049
-// rows, D = 256 in fp32, 8 warps: 36 us, and 24 split.)
-constexpr int kShortUnits = 16;
-constexpr int kMaxBlocks = 1024;  // of the attention kernel (four to an SM at most)
-// Where the rows of its blocks begin in the units, in 128ths, by resident
-// blocks to an SM (see Runs).
-constexpr int kZones[4][4] = {{0, 0, 0, 0}, {0, 64, 0, 0}, {0, 43, 86, 0}, {0, 32, 64, 96}};
-
 // Query tiles (of 8 columns) of an item: as many as the rows of a key/value
 // head fill, as the register budget allows (the query operand and the sums of
 // a tile take D/16 * (2 * parts + 4) registers).
@@ -233,13 +154,6 @@ int query_tiles(int dtype, int D, int64_t rows)
     while (nt < 4 && rows > 8 * nt && 2 * nt * (D / 16) * (2 * parts + 4) <= 192) nt *= 2;
     return nt;
 }
-
-struct AttentionPlan {
-    int nt, log_rows, max_items;
-    bool whole;  // items may go to one block each
-    int64_t max_units;  // of an item
-    int64_t runs, part, part_ml, row_ml, logits, bytes;  // offsets in the workspace, and its size
-};
 
 AttentionPlan attention_plan(int64_t B, int dtype, int Hq, int Hk, int D, int max_q,
                              int64_t max_kv, bool scores)
@@ -270,77 +184,6 @@ AttentionPlan attention_plan(int64_t B, int dtype, int Hq, int Hk, int D, int ma
     p.bytes = at > INT64_MAX ? INT64_MAX : (int64_t)at;
     return p;
 }
-
-template <typename TS, int D, int NT, int kWarps>
-int launch_whole(const AttentionArgs &a, const AttentionPlan &p, int sms, cudaStream_t stream,
-                 bool *done)
-{
-    static std::atomic<int> cache[kMaxDevices];
-    constexpr int smem = kAttentionSmem<D, NT, kQueryParts<TS>, kWarps>;
-    auto kern = qkn_kv4_attention_kernel<TS, D, NT, kWarps>;
-    int per_sm = 0, rc;
-    if ((rc = blocks_per_sm(kern, kWarps * 32, smem, cache, &per_sm)) != QKN_OK) return rc;
-    const int64_t items = a.B * (int64_t)p.max_items, room = (int64_t)sms * per_sm;
-    const int64_t most = p.max_units - kItemUnits;
-    *done = (items <= room && most <= kWarps * kWarps / 2) ||
-            (items <= 2 * room && most <= kShortUnits);
-    if (!*done) return QKN_OK;
-    return launch(kern, dim3((unsigned)items), kWarps * 32, smem, stream, a);
-}
-
-template <typename TS, int D, int NT>
-int launch_attention(const AttentionArgs &a, const AttentionPlan &p, cudaStream_t stream)
-{
-    int per_sm = 0, sms = 0, rc;
-    if ((rc = device_sms(&sms)) != QKN_OK) return rc;
-    if (p.whole) {
-        // The most warps that the registers (and shared memory) of an SM hold.
-        bool done = false;
-        if constexpr (kRunBlocks<TS, D, NT> == 4)
-            if ((rc = launch_whole<TS, D, NT, 16>(a, p, sms, stream, &done)) != QKN_OK || done)
-                return rc;
-        if constexpr (D < 256 || NT == 1)
-            if ((rc = launch_whole<TS, D, NT, 8>(a, p, sms, stream, &done)) != QKN_OK || done)
-                return rc;
-    }
-    static std::atomic<int> cache[kMaxDevices];
-    constexpr int smem = kAttentionSmem<D, NT, kQueryParts<TS>, kRunWarps>;
-    auto kern = qkn_kv4_attention_kernel<TS, D, NT, kRunWarps>;
-    if ((rc = blocks_per_sm(kern, kRunThreads, smem, cache, &per_sm)) != QKN_OK) return rc;
-    const int64_t units = (int64_t)a.B * p.max_items * p.max_units;
-    if (per_sm > 4) per_sm = 4;
-    if ((int64_t)sms * per_sm > kMaxBlocks) return QKN_ERR_UNSUPPORTED;
-    // Whole rows of blocks, one on every SM; fewer blocks where the call cannot
-    // have a unit for each.
-    dim3 shape((unsigned)sms, (unsigned)per_sm);
-    if (units < (int64_t)sms * per_sm) shape = dim3((unsigned)units, 1u);
-    AttentionArgs args = a;
-    for (int y = 0; y < 4; ++y) args.zones[y] = kZones[per_sm - 1][y];
-    const unsigned blocks = shape.x * shape.y;
-    if ((rc = launch(kern, shape, kRunThreads, smem, stream, args)) != QKN_OK) return rc;
-    rc = launch(qkn_kv4_join_kernel<TS, D, 8 * NT>, dim3(blocks, 8 * NT / kJoinRows), kJoinThreads,
-                0, stream, args);
-    if (rc != QKN_OK || a.scores == nullptr) return rc;
-    return launch(qkn_kv4_scores_kernel<8 * NT>, dim3(blocks, kScoreSplit), kScoreThreads, 0, stream,
-                  args);
-}
-
-struct Attention {
-    template <typename TS, int D>
-    static int run(AttentionArgs a, AttentionPlan p, cudaStream_t stream)
-    {
-        constexpr int kTile = D / 16 * (2 * kQueryParts<TS> + 4);
-#define QKN_KV4_NT(NT)                                                                         \
-    if constexpr (NT == 1 || NT * kTile <= 192)                                                \
-        if (p.nt == NT)                                                                        \
-            return launch_attention<TS, D, NT>(a, p, stream);
-        QKN_KV4_NT(1)
-        QKN_KV4_NT(2)
-        QKN_KV4_NT(4)
-#undef QKN_KV4_NT
-        return QKN_ERR_UNSUPPORTED;
-    }
-};
 
 // ---------------------------------------------------------------- eviction --
 // Rows of a head that a cluster holds at most: 80 to a thread, 8 blocks.
@@ -531,7 +374,13 @@ int qknorm_kv4_attention(const void *q, int dtype, int64_t T, int Hq, int Hk, in
     a.part_ml = reinterpret_cast<float2 *>(ws + plan.part_ml);
     a.row_ml = reinterpret_cast<float2 *>(ws + plan.row_ml);
     a.logits = reinterpret_cast<float *>(ws + plan.logits);
-    return by_type<Attention>(dtype, D, a, plan, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    switch (dtype) {
+    case QKN_BF16: return qkn_kv4_attention_bf16(D, &a, &plan, s);
+    case QKN_FP32: return qkn_kv4_attention_fp32(D, &a, &plan, s);
+    case QKN_FP16: return qkn_kv4_attention_fp16(D, &a, &plan, s);
+    default: return qkn_kv4_attention_e4m3(D, &a, &plan, s);
+    }
 }
 
 int qknorm_kv4_evict(void *pool, int64_t num_pages, int page_size, int Hk, int D, float *scores,
@@ -583,7 +432,15 @@ int qknorm_kv4_bad_pages(unsigned int *count)
 {
     if (count == nullptr) return QKN_ERR_NULL;
     const cudaError_t e = cudaMemcpyFromSymbol(count, g_kv4_bad_pages, sizeof(unsigned int));
-    return e == cudaSuccess ? QKN_OK : cuda_fail(e);
+    if (e != cudaSuccess) return cuda_fail(e);
+    unsigned int n = 0;
+    int rc;
+#define QKN_KV4_ADD(NAME)                                                                      \
+    if ((rc = qkn_kv4_bad_pages_##NAME(&n)) != QKN_OK) return rc;                              \
+    *count += n;
+    QKN_KV4_TYPES(QKN_KV4_ADD)
+#undef QKN_KV4_ADD
+    return QKN_OK;
 }
 
 int qknorm_kv4_last_cuda_error(void) { return g_last_error; }
