@@ -356,7 +356,7 @@ template <>
 constexpr int kWeightParts<__nv_fp8_e4m3> = 1;
 // Values as raw codes: a unit's sums get -8 times its weights on fp32 pairs,
 // D/8 instructions where centring the operands takes D/2.  That pays while
-// there is one query tile and one part.
+// there is one query tile; an fp16 or fp32 output would show the lost bits.
 template <typename TS, int NT>
 constexpr bool kRawValues = NT == 1 && kWeightParts<TS> == 1;
 
@@ -453,6 +453,42 @@ constexpr float kLeastScale = 7.7037197e-34f;  // 2^-110
 // lanes on a bank: tile row r is the block's row row_of(r).
 __device__ __forceinline__ int row_of(int r) { return (r >> 1) + 4 * (r & 1); }
 
+// Adds to add[v] the weights of `rows` query rows for the cached rows whose
+// logit records lie `stride` apart from x on (at[v] < 0: none); ml(r) is a
+// query row's maximum and 1 / sum.  A record is two logits, or fours of them.
+template <int kBatch, typename Ml>
+__device__ __forceinline__ void weigh_logits(const float *x, int stride, int log_rows, int rows,
+                                             const int64_t (&at)[kBatch], float (&add)[kBatch],
+                                             Ml ml)
+{
+    for (int r = 0; r < rows; r += 4) {
+        float4 y[kBatch];
+#pragma unroll
+        for (int v = 0; v < kBatch; ++v) {
+            y[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (at[v] < 0) continue;
+            const float *p = x + (int64_t)v * stride + r;
+            if (log_rows > 2) {
+                y[v] = *reinterpret_cast<const float4 *>(p);
+            } else {
+                const float2 two = *reinterpret_cast<const float2 *>(p);
+                y[v].x = two.x;
+                y[v].y = two.y;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (r + e >= rows) break;
+            const float2 f = ml(r + e);
+#pragma unroll
+            for (int v = 0; v < kBatch; ++v) {
+                const float z = e == 0 ? y[v].x : (e == 1 ? y[v].y : (e == 2 ? y[v].z : y[v].w));
+                add[v] = fmaf(exp2_approx(z - f.x), f.y, add[v]);
+            }
+        }
+    }
+}
+
 // Adds to the scores of a head's n cached rows the weights that its query
 // rows' logits give (row j's records start at record `first` * kUnitRows + j),
 // a thread to a row, kBatch rows in flight; ml: each query row's maximum and
@@ -480,18 +516,8 @@ __device__ __forceinline__ void add_scores(const AttentionArgs &a, int b, int hk
 #pragma unroll
         for (int v = 0; v < kBatch; ++v) old[v] = at[v] >= 0 ? a.scores[at[v]] : 0.f;
         const float *x = a.logits + ((int64_t)first * kUnitRows + j0) * a.log_rows;
-        for (int r = 0; r < rows; r += 2) {
-            const bool two = r + 1 < rows;
-            const float2 f = ml[r], f1 = two ? ml[r + 1] : make_float2(0.f, 0.f);
-#pragma unroll
-            for (int v = 0; v < kBatch; ++v) {
-                if (at[v] < 0) continue;
-                const float2 y = *reinterpret_cast<const float2 *>(
-                    x + (int64_t)v * kThreads * a.log_rows + r);
-                add[v] = fmaf(exp2_approx(y.x - f.x), f.y, add[v]);
-                if (two) add[v] = fmaf(exp2_approx(y.y - f1.x), f1.y, add[v]);
-            }
-        }
+        weigh_logits(x, kThreads * a.log_rows, a.log_rows, rows, at, add,
+                     [&](int r) { return ml[r]; });
 #pragma unroll
         for (int v = 0; v < kBatch; ++v)
             if (at[v] >= 0) a.scores[at[v]] = old[v] + add[v];
@@ -1237,23 +1263,13 @@ __global__ void __launch_bounds__(kScoreThreads) qkn_kv4_scores_kernel(const Att
                 }
 #pragma unroll
                 for (int v = 0; v < kBatch; ++v) old[v] = at[v] >= 0 ? a.scores[at[v]] : 0.f;
-                for (int tile = 0, r = 0; r < rows; ++tile) {
-                    const float *xt = x + tile * tile_stride;
-                    for (const int end = min(rows, r + kR); r < end; r += 2) {
-                        const int qi = r / a.group, qj = (r + 1) / a.group;
-                        const bool two = r + 1 < rows;
-                        const float2 f = ml[qi * a.Hq + r - qi * a.group];
-                        const float2 f1 =
-                            two ? ml[qj * a.Hq + r + 1 - qj * a.group] : make_float2(0.f, 0.f);
-#pragma unroll
-                        for (int v = 0; v < kBatch; ++v) {
-                            if (at[v] < 0) continue;
-                            const float2 y = *reinterpret_cast<const float2 *>(
-                                xt + v * kUnitRows * a.log_rows + r % kR);
-                            add[v] = fmaf(exp2_approx(y.x - f.x), f.y, add[v]);
-                            if (two) add[v] = fmaf(exp2_approx(y.y - f1.x), f1.y, add[v]);
-                        }
-                    }
+                for (int tile = 0; tile * kR < rows; ++tile) {
+                    const int here = min(kR, rows - tile * kR);
+                    weigh_logits(x + tile * tile_stride, kUnitRows * a.log_rows, a.log_rows, here, at,
+                                 add, [&](int r) {
+                                     const int qr = tile * kR + r, qi = qr / a.group;
+                                     return ml[qi * a.Hq + qr - qi * a.group];
+                                 });
                 }
 #pragma unroll
                 for (int v = 0; v < kBatch; ++v)

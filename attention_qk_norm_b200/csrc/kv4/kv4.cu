@@ -166,7 +166,7 @@ AttentionPlan attention_plan(int64_t B, int dtype, int Hq, int Hk, int D, int ma
     p.max_units = (max_kv + kUnitRows - 1) / kUnitRows + kItemUnits;
     p.max_items = (int)(tiles * Hk);
     p.whole = (!scores || tiles == 1) && B * tiles * Hk <= INT32_MAX;
-    p.log_rows = (int)(rows < kr ? (rows + 1) / 2 * 2 : kr);
+    p.log_rows = (int)(rows <= 2 ? 2 : (rows < kr ? (rows + 3) / 4 * 4 : kr));
     // Sizes may pass 63 bits for arguments that no buffer could have.
     __int128 at = 0;
     p.runs = 0;
