@@ -290,9 +290,14 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel)
+// Two 16x16 tiles of bytes, transposed: lane 4 g + t gets, of each tile, rows
+// 4 t .. 4 t + 3 of column g and of column g + 8.
+__device__ __forceinline__ void load_transposed(uint32_t (&w)[4], uint32_t row)
 {
-    return __byte_perm(a, b, sel);
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(row)
+                 : "memory");
 }
 
 // The four pairs (nibble p, nibble p + 4), p = 0..3, of a word of codes as
@@ -449,10 +454,8 @@ constexpr int kWeightExp = 6;
 constexpr float kLag = 8.f;
 constexpr float kLeastScale = 7.7037197e-34f;  // 2^-110
 
-// Rows of the 16-row tile in an order that lets a warp read V with at most two
-// lanes on a bank: tile row r is the block's row row_of(r).
-__device__ __forceinline__ int row_of(int r) { return (r >> 1) + 4 * (r & 1); }
-
+// Tile rows g and g + 8 (and so columns of the second product) are the block's
+// rows 2 g and 2 g + 1, the order in which V's transposed bytes pair them.
 // Adds to add[v] the weights of `rows` query rows for the cached rows whose
 // logit records lie `stride` apart from x on (at[v] < 0: none); ml(r) is a
 // query row's maximum and 1 / sum.  A record is two logits, or fours of them.
@@ -544,7 +547,6 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
     constexpr int kMTiles = D / 16;
     const bool scored = a.scores != nullptr;
     constexpr int kKWords = D / 32;  // a lane's words of a K row
-    constexpr int kVWords = D / 64;  // a lane's words of a V row
     constexpr int kS = kStages<D>;
     constexpr int kBB = kBlockBytes<D>;
     constexpr int kChunks = kBB / 16;
@@ -747,7 +749,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const uint8_t *p =
-                        unit + half * kBB + (row_of(g) + 8 * r) * (D / 2) + t * (D / 8);
+                        unit + half * kBB + (2 * g + r) * (D / 2) + t * (D / 8);
                     if constexpr (kKWords == 2) {
                         const uint2 u = *reinterpret_cast<const uint2 *>(p);
                         kw[half][r][0] = u.x;
@@ -792,13 +794,15 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
             float vs[2][2], vm[2][2];
 #pragma unroll
             for (int half = 0; half < 2; ++half)
+{
+                const uint8_t *par = unit + half * kBB + 16 * D + g * 8;
+                const uint2 kp = *reinterpret_cast<const uint2 *>(par);
+                const uint2 vp = *reinterpret_cast<const uint2 *>(par + 64);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const uint8_t *par = unit + half * kBB + 16 * D + (row_of(g) + 8 * r) * 4;
                     float ks, km;
-                    unpack_params(*reinterpret_cast<const uint32_t *>(par), ks, km);
-                    unpack_params(*reinterpret_cast<const uint32_t *>(par + 64), vs[half][r],
-                                  vm[half][r]);
+                    unpack_params(r ? kp.y : kp.x, ks, km);
+                    unpack_params(r ? vp.y : vp.x, vs[half][r], vm[half][r]);
                     if constexpr (kRawK) km = fmaf(-8.f, ks, km);
                     ks *= c_s;
 #pragma unroll
@@ -808,6 +812,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                             s[half][nt][2 * r + e] =
                                 fmaf(ks, s[half][nt][2 * r + e], km * qsum[nt][e]);
                 }
+            }
             // Rows that are hidden from some of the queries, or from all.
             const uint32_t bad_here = (bad >> (2 * stage)) & 3u;
             const bool masked = base + kUnitRows > all_see || bad_here != 0;
@@ -816,7 +821,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const int j = base + half * kBlockRows + row_of(g) + 8 * r;
+                        const int j = base + half * kBlockRows + 2 * g + r;
                         const bool gone = j >= seq.n || (bad_here >> half & 1u);
                         if (gone) vs[half][r] = vm[half][r] = 0.f;
 #pragma unroll
@@ -842,7 +847,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                             top[nt][e] = fmaxf(top[nt][e], s[half][nt][2 * r + e]);
                     if (scored) {
                         float *to = a.logits + ((int64_t)(first + at + k) * kUnitRows + half * kBlockRows +
-                                                row_of(g) + 8 * r) * a.log_rows;
+                                                2 * g + r) * a.log_rows;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             if (nt * 8 + 2 * t < a.log_rows)
@@ -945,8 +950,10 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
                         for (int r = 0; r < 2; ++r)
                             wf[half][nt][part][r] = transpose8x8(wf[half][nt][part][r]);
 
-            // O^T += V^T W^T: operand rows g and g + 8 of m-tile 4 * v + p are
-            // elements p and p + 4 of the lane's word v.  With raw codes, 8 times
+            // O^T += V^T W^T: V's bytes come transposed, 4 rows of a byte column to
+            // a word.  Operand rows g and g + 8 of m-tile 2 * c are the even elements
+            // of byte columns 16 * c + g and + 8, m-tile 2 * c + 1 has the odd ones.
+            // With raw codes, 8 times
             // the unit's weights are taken off every sum: their own sums come
             // from a product with ones.
             if constexpr (kRawV) {
@@ -969,41 +976,26 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const uint8_t *blk = unit + half * kBB + 8 * D + g * (D / 16);
-                uint32_t vw[4][kVWords];
+                const uint32_t rows = smem_u32(unit + half * kBB + 8 * D) +
+                                      lane % 16 * (D / 2) + lane / 16 * 16;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint8_t *p = blk + (t + 4 * r) * (D / 2);
-                    if constexpr (kVWords == 1) {
-                        vw[r][0] = *reinterpret_cast<const uint32_t *>(p);
-                    } else if constexpr (kVWords == 2) {
-                        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-                        vw[r][0] = u.x;
-                        vw[r][1] = u.y;
-                    } else {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-                        vw[r][0] = u.x;
-                        vw[r][1] = u.y;
-                        vw[r][2] = u.z;
-                        vw[r][3] = u.w;
+                for (int v = 0; v < D / 64; ++v) {
+                    uint32_t w4[4];
+                    load_transposed(w4, rows + v * 32);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t x0[4], x1[4];
+                        unpack_nibbles<kRawV>(w4[2 * i], x0);
+                        unpack_nibbles<kRawV>(w4[2 * i + 1], x1);
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int part = 0; part < kWP; ++part)
+                                    mma(acc[4 * v + 2 * i + p][nt], x0[p], x1[p], x0[p + 2],
+                                        x1[p + 2], wf[half][nt][part][0], wf[half][nt][part][1]);
                     }
-                }
-#pragma unroll
-                for (int v = 0; v < kVWords; ++v) {
-                    uint32_t x0[4], x1[4], x2[4], x3[4];
-                    unpack_nibbles<kRawV>(prmt(vw[0][v], vw[1][v], 0x5410), x0);
-                    unpack_nibbles<kRawV>(prmt(vw[0][v], vw[1][v], 0x7632), x1);
-                    unpack_nibbles<kRawV>(prmt(vw[2][v], vw[3][v], 0x5410), x2);
-                    unpack_nibbles<kRawV>(prmt(vw[2][v], vw[3][v], 0x7632), x3);
-#pragma unroll
-                    for (int p = 0; p < 4; ++p)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int part = 0; part < kWP; ++part) {
-                                const uint32_t b0 = wf[half][nt][part][0], b1 = wf[half][nt][part][1];
-                                mma(acc[4 * v + p][nt], x0[p], x1[p], x2[p], x3[p], b0, b1);
-                            }
                 }
             }
         };
@@ -1029,16 +1021,14 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int col = nt * 8 + 2 * t + e;
-                    float *to = join + (warp * kR + col) * (D + 4) + g * (D / 8);
+                    float *to = join + (warp * kR + col) * (D + 4) + 2 * g;
 #pragma unroll
-                    for (int v = 0; v < kVWords; ++v)
+                    for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-                        for (int hi = 0; hi < 2; ++hi) {
-                            const int c = 2 * hi + e;
-                            *reinterpret_cast<float4 *>(to + v * 8 + hi * 4) = make_float4(
-                                acc[4 * v][nt][c] * kEven, acc[4 * v + 1][nt][c] * kOdd,
-                                acc[4 * v + 2][nt][c] * kEven, acc[4 * v + 3][nt][c] * kOdd);
-                        }
+                        for (int hi = 0; hi < 2; ++hi)
+                            *reinterpret_cast<float2 *>(to + 32 * c + 16 * hi) =
+                                make_float2(acc[2 * c][nt][2 * hi + e] * kEven,
+                                            acc[2 * c + 1][nt][2 * hi + e] * kOdd);
 #pragma unroll
                     for (int o = 4; o < 32; o *= 2) {
                         l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
