@@ -56,7 +56,6 @@ struct AttentionArgs {
     float *scores;
     // Launch shape and workspace.
     int max_units;     // units of an item at most
-    int zones[4];      // where each row of blocks begins in the units, in 128ths
     int max_items;     // items of a sequence at most
     int log_rows;      // query rows of a logit record
     RunRecord *runs;   // [blocks]
@@ -95,10 +94,11 @@ __device__ __forceinline__ void q_range(const AttentionArgs &a, int b, int &star
 // splits as evenly as one of equal ones.  Every item counts kItemUnits empty
 // units behind its own, the time that a block spends on an item beside its
 // units (measured on B200: without them a block with many short items came
-// last by 20 us of 97 for 64 sequences of 37 to 8192 rows); a run that would
-// end among them ends behind them.
+// last by 20 us of 97 for 64 sequences of 37 to 8192 rows; 2, 4 and 8 of them
+// give 81, 77 and 75 us there and 23, 19.6 and 21 for 7 sequences of 1 to 2049
+// rows in fp32 with D = 256); a run that would end among them ends behind them.
 constexpr int kUnitRows = 32;
-constexpr int kItemUnits = 4;
+constexpr int kItemUnits = 6;
 constexpr int kRunWarps = 4;  // of a block that takes a run of units
 constexpr int kRunThreads = kRunWarps * 32;
 
@@ -146,49 +146,26 @@ struct Walk {
     }
 };
 
-// The blocks' runs.  The grid is the resident blocks, a row of it (y) one block
-// on every SM, started in this order, and an SM's schedulers prefer the warps
-// that started first: with equal runs the rows' blocks ended after 75, 82, 91
-// and 99 us of a call, the SM half empty towards the end.  So a row's share of
-// the units falls with y (a.zones); its blocks share it equally.  Calls of a
-// few units a block are split equally among all blocks.
-constexpr uint32_t kEvenUnits = 12;
-
+// The blocks' runs: equal shares of the call's units.  (An SM's schedulers
+// prefer the warps that started first, so that the four blocks of an SM end one
+// after the other; larger shares for the first ones made them end together and
+// the call 2% longer.)
 struct Runs {
-    uint32_t total, blocks;
-    bool even;
-    __device__ __forceinline__ Runs(uint32_t units)
+    uint32_t each, rest;  // units of a block, and blocks with one more
+    __device__ __forceinline__ Runs(uint32_t total)
     {
-        total = units;
-        blocks = gridDim.x * gridDim.y;
-        even = gridDim.y == 1 || units < kEvenUnits * blocks;
+        each = total / gridDim.x;
+        rest = total - each * gridDim.x;
     }
-    __device__ __forceinline__ uint32_t zone(const AttentionArgs &a, uint32_t y) const
+    __device__ __forceinline__ uint32_t begin(uint32_t block) const
     {
-        return y < gridDim.y ? (uint32_t)((uint64_t)total * (uint32_t)a.zones[y] >> 7) : total;
-    }
-    // First unit of block x of row y (x == gridDim.x: of the next row).
-    __device__ __forceinline__ uint32_t begin(const AttentionArgs &a, uint32_t x, uint32_t y) const
-    {
-        const uint32_t from = even ? 0 : zone(a, y), n = even ? total : zone(a, y + 1) - from;
-        const uint32_t among = even ? blocks : gridDim.x, id = even ? y * gridDim.x + x : x;
-        const uint32_t each = n / among, rest = n - each * among;
-        return from + id * each + min(id, rest);
+        return block * each + min(block, rest);
     }
     // The block whose run holds unit u.
-    __device__ __forceinline__ uint32_t holder(const AttentionArgs &a, uint32_t u) const
+    __device__ __forceinline__ uint32_t holder(uint32_t u) const
     {
-        uint32_t y = 0, from = 0, n = total, among = blocks;
-        if (!even) {
-            while (y + 1 < gridDim.y && u >= zone(a, y + 1)) ++y;
-            from = zone(a, y);
-            n = zone(a, y + 1) - from;
-            among = gridDim.x;
-        }
-        u -= from;
-        const uint32_t each = n / among, rest = n - each * among;
-        const uint32_t id = u < rest * (each + 1) ? u / (each + 1) : rest + (u - rest * (each + 1)) / each;
-        return y * gridDim.x + id;
+        const uint32_t more = rest * (each + 1);
+        return u < more ? u / (each + 1) : rest + (u - more) / each;
     }
 };
 
@@ -228,7 +205,7 @@ __device__ __forceinline__ uint32_t block_run(const AttentionArgs &a, uint32_t *
     const Runs runs(total);
 #pragma unroll 1
     for (int side = 0; side < 2; ++side) {
-        const uint32_t at = runs.begin(a, blockIdx.x + side, blockIdx.y);
+        const uint32_t at = runs.begin(blockIdx.x + side);
         if (at >= before && at < before + mine) {
             uint32_t seen = before;
             int b = b0;
@@ -566,7 +543,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
     Walk<kR> w;
     uint32_t first = 0, all = 0;
     int total = 0;
-    const int block = (int)(blockIdx.y * gridDim.x + blockIdx.x);
+    const int block = (int)blockIdx.x;
     if constexpr (kWhole) {
         w.b = blockIdx.x / a.max_items;
         w.item = blockIdx.x - w.b * a.max_items;
@@ -1100,7 +1077,7 @@ qkn_kv4_attention_kernel(const AttentionArgs a)
             rec.join_b = w.b;
             rec.join_item = w.item;
             rec.join_slot = slot;
-            rec.join_last = (int)Runs(all).holder(a, first + at + w.units - kItemUnits - 1);
+            rec.join_last = (int)Runs(all).holder(first + at + w.units - kItemUnits - 1);
         }
         __syncthreads();
         at += seg_units;

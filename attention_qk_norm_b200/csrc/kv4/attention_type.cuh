@@ -13,10 +13,6 @@ namespace {
 // 500 to 2500 rows, D = 128: 14.7 us, and 20.7 split; 28 heads of 1 to 2049
 // rows, D = 256 in fp32, 8 warps: 36 us, and 24 split.)
 constexpr int kShortUnits = 16;
-// Where the rows of its blocks begin in the units, in 128ths, by resident
-// blocks to an SM (see Runs).
-constexpr int kZones[4][4] = {{0, 0, 0, 0}, {0, 64, 0, 0}, {0, 43, 86, 0}, {0, 32, 64, 96}};
-
 template <typename TS, int D, int NT, int kWarps>
 int launch_whole(const AttentionArgs &a, const AttentionPlan &p, int sms, cudaStream_t stream,
                  bool *done)
@@ -54,21 +50,15 @@ int launch_attention(const AttentionArgs &a, const AttentionPlan &p, cudaStream_
     auto kern = qkn_kv4_attention_kernel<TS, D, NT, kRunWarps>;
     if ((rc = blocks_per_sm(kern, kRunThreads, smem, cache, &per_sm)) != QKN_OK) return rc;
     const int64_t units = (int64_t)a.B * p.max_items * p.max_units;
-    if (per_sm > 4) per_sm = 4;
-    if ((int64_t)sms * per_sm > kMaxBlocks) return QKN_ERR_UNSUPPORTED;
-    // Whole rows of blocks, one on every SM; fewer blocks where the call cannot
-    // have a unit for each.
-    dim3 shape((unsigned)sms, (unsigned)per_sm);
-    if (units < (int64_t)sms * per_sm) shape = dim3((unsigned)units, 1u);
-    AttentionArgs args = a;
-    for (int y = 0; y < 4; ++y) args.zones[y] = kZones[per_sm - 1][y];
-    const unsigned blocks = shape.x * shape.y;
-    if ((rc = launch(kern, shape, kRunThreads, smem, stream, args)) != QKN_OK) return rc;
-    rc = launch(qkn_kv4_join_kernel<TS, D, 8 * NT>, dim3(blocks, 8 * NT / kJoinRows), kJoinThreads,
-                0, stream, args);
+    int64_t blocks = (int64_t)sms * per_sm;
+    if (blocks > kMaxBlocks) blocks = kMaxBlocks;
+    if (blocks > units) blocks = units;
+    if ((rc = launch(kern, dim3((unsigned)blocks), kRunThreads, smem, stream, a)) != QKN_OK) return rc;
+    rc = launch(qkn_kv4_join_kernel<TS, D, 8 * NT>, dim3((unsigned)blocks, 8 * NT / kJoinRows),
+                kJoinThreads, 0, stream, a);
     if (rc != QKN_OK || a.scores == nullptr) return rc;
-    return launch(qkn_kv4_scores_kernel<8 * NT>, dim3(blocks, kScoreSplit), kScoreThreads, 0, stream,
-                  args);
+    return launch(qkn_kv4_scores_kernel<8 * NT>, dim3((unsigned)blocks, kScoreSplit), kScoreThreads, 0,
+                  stream, a);
 }
 
 template <int D>
