@@ -65,11 +65,11 @@ template <int D>
 int run_attention(const AttentionArgs &a, const AttentionPlan &p, cudaStream_t stream)
 {
     using TS = QKN_KV4_TYPE;
-    constexpr int kTile = D / 16 * (2 * kQueryParts<TS> + 4);
+    constexpr bool kFp32 = sizeof(TS) == 4;
     if (p.nt == 1) return launch_attention<TS, D, 1>(a, p, stream);
-    if constexpr (2 * kTile <= 192)
+    if constexpr (tiles_fit(D, kFp32, 2))
         if (p.nt == 2) return launch_attention<TS, D, 2>(a, p, stream);
-    if constexpr (4 * kTile <= 192)
+    if constexpr (tiles_fit(D, kFp32, 4))
         if (p.nt == 4) return launch_attention<TS, D, 4>(a, p, stream);
     return QKN_ERR_UNSUPPORTED;
 }

@@ -90,6 +90,13 @@ int blocks_per_sm(Kern kern, int threads, int smem, std::atomic<int> *cache, int
 
 constexpr int kMaxBlocks = 1024;  // of the attention kernel (four to an SM at most)
 
+// Whether the registers hold a number of query tiles: a tile's sums and its
+// share of the products' operands take D/16 * (4 + 2 * parts).
+constexpr bool tiles_fit(int D, bool fp32, int tiles)
+{
+    return tiles * (D / 16) * (fp32 ? 8 : 6) <= (tiles > 2 ? 128 : 192);
+}
+
 struct AttentionPlan {
     int nt, log_rows, max_items;
     bool whole;  // items may go to one block each

@@ -145,13 +145,14 @@ struct Read {
 
 // -------------------------------------------------------------- attention --
 // Query tiles (of 8 columns) of an item: as many as the rows of a key/value
-// head fill, as the register budget allows (the query operand and the sums of
-// a tile take D/16 * (2 * parts + 4) registers).
+// head fill, as registers allow.  Two tiles against one, 16 rows or more to a
+// head: 50 us and 58 (D = 128), 37 and 39 (256), fp32 27 and 30; four against
+// two: 52 and 52 (64), fp32 64 and 74, but 85 and 82 at D = 128, where four do
+// not fit.
 int query_tiles(int dtype, int D, int64_t rows)
 {
-    const int parts = dtype == QKN_FP32 ? 2 : 1;
     int nt = 1;
-    while (nt < 4 && rows > 8 * nt && 2 * nt * (D / 16) * (2 * parts + 4) <= 192) nt *= 2;
+    while (nt < 4 && rows > 8 * nt && tiles_fit(D, dtype == QKN_FP32, 2 * nt)) nt *= 2;
     return nt;
 }
 
