@@ -260,6 +260,7 @@ int attention_shape(int64_t B, int dtype, int Hq, int Hk, int D, int max_q, int6
     if (B < 0 || B > 65535 || Hk < 1 || Hq < 1 || Hq > 65535 || Hq % Hk != 0 || max_q < 1 ||
         max_q > 65535 || max_kv < 0 || max_kv > INT32_MAX)
         return QKN_ERR_SHAPE;
+    if ((int64_t)max_q * (Hq / Hk) > 1 << 30) return QKN_ERR_SHAPE;
     return QKN_OK;
 }
 
@@ -345,8 +346,8 @@ int qknorm_kv4_attention(const void *q, int dtype, int64_t T, int Hq, int Hk, in
     const AttentionPlan plan =
         attention_plan(B, dtype, Hq, Hk, D, max_q, max_pages * page_size, scores != nullptr);
     if (workspace_bytes < plan.bytes) return QKN_ERR_SHAPE;
-    if ((__int128)B * plan.max_items * plan.max_units > INT32_MAX)
-        return QKN_ERR_SHAPE;
+    // Units are numbered in 32 bits.
+    if ((__int128)B * plan.max_items * plan.max_units > INT32_MAX) return QKN_ERR_SHAPE;
     AttentionArgs a = {};
     a.q = q;
     a.T = T;

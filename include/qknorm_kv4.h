@@ -114,7 +114,12 @@ int qknorm_kv4_read(const void *pool, int64_t num_pages, int page_size, int Hk, 
  *
  * workspace: device memory, 16-byte aligned, of at least the bytes that
  * qknorm_kv4_attention_workspace gives for the same B, heads, D, dtype, max_q,
- * max_pages * page_size and scores != NULL.
+ * max_kv = max_pages * page_size and with_scores = (scores != NULL); with
+ * scores that is about 4 bytes for each query row and cached row the tables can
+ * name.  QKN_ERR_SHAPE for a smaller one, and for calls of more than 2^31 units
+ * of 32 cached rows of one key/value head and 8 to 32 query rows.
+ *
+ * Results do not depend on timing: the same call gives the same bits.
  */
 int qknorm_kv4_attention(const void *q, int dtype, int64_t T, int Hq, int Hk, int D,
                          int64_t row_stride, const void *pool, int64_t num_pages, int page_size,
@@ -135,7 +140,9 @@ int qknorm_kv4_attention_workspace(int64_t B, int dtype, int Hq, int Hk, int D, 
  * ... of the pages dst_table[b * dst_stride + 0 .. dst_pages) names, which
  * must not be among the pages read; the old pages are the caller's to reuse.
  * new_lens[b] becomes min(n, budget), and kept[b][h][0 .. budget) the kept
- * rows' numbers, -1 behind the last.  dst_pages * page_size >= budget >= 1.
+ * rows' numbers, -1 behind the last.  new_lens must not be kv_lens (other heads'
+ * blocks still read it).  scores is 16-byte aligned.
+ * dst_pages * page_size >= budget >= 1.
  */
 int qknorm_kv4_evict(void *pool, int64_t num_pages, int page_size, int Hk, int D, float *scores,
                      const int32_t *page_table, int64_t table_stride, int64_t max_pages,

@@ -116,6 +116,10 @@ def test_attention_workspace(lib):
     # Enough is accepted (the call then meets the next check), one byte less is not.
     assert attention(lib, wsb=small - 1) == SHAPE
     assert w(65535, FP32, 128, 8, 256, 65535, 2 ** 31 - 256, 1, n) == OK and n.value > 0
+    # More rows or units than 32-bit numbers hold: refused before anything is touched.
+    assert w(1, BF16, 65535, 1, 64, 65535, 256, 0, n) == SHAPE
+    big = dict(B=60000, T=60000, maxp=1 << 20, tstride=1 << 20, wsb=2 ** 62)
+    assert attention(lib, **big) == SHAPE
 
 
 def test_evict_validation(lib):

@@ -253,6 +253,45 @@ def test_attention_long(B, n, Hq, Hk, D, page):
     assert torch.equal(sums, cache.scores)  # the same bits on every run
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens", [[700], [33] * 70, [5, 4000, 900, 1] * 3])
+def test_whole_items_and_split_items_agree(dtype, lens):
+    """The same call with a table of its own width and with a wide one (which
+    decides whether an item goes to one block), both against the plain form."""
+    B = len(lens)
+    for scores in (False, True):
+        cache, q, table, starts = problem(B, lens, [1] * B, 8, 2, 128, 64, dtype, scores)
+        if scores:
+            cache.scores.uniform_(0, 2)
+        first = None if not scores else cache.scores.clone()
+        dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        for pad in (0, 3000):
+            wide = torch.cat([table, torch.full((B, pad), -1, dtype=torch.int32)], 1)
+            if scores:
+                cache.scores.copy_(first)
+            out, lse = qkn.qknorm_kv4_attention(cache, q, 8, wide.cuda(), dl, add_scores=scores)
+            check(cache, q, 8, table, lens, starts, dtype, out, lse,
+                  scores_before=first.cpu().numpy() if scores else None)
+
+
+def test_attention_without_lse_through_the_c_entry():
+    lens = [300, 17]
+    cache, q, table, starts = problem(2, lens, [1, 1], 4, 2, 64, 16, "fp16")
+    dl, dt = torch.tensor(lens, dtype=torch.int32, device="cuda"), table.cuda()
+    ws = qkn.kv4_attention_workspace(cache, q, 4, dt)
+    out = torch.empty(2, 256, dtype=torch.float16, device="cuda")
+    rc = qkn._kv4._lib().qknorm_kv4_attention(
+        q.data_ptr(), 2, 2, 4, 2, 64, q.stride(0), cache.pool.data_ptr(), cache.num_pages, 16,
+        dt.data_ptr(), dt.stride(0), dt.shape[1], dl.data_ptr(), 2, None, 1, 0.125, out.data_ptr(),
+        256, None, None, ws.data_ptr(), ws.nbytes, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    want, lse = qkn.qknorm_kv4_attention(cache, q, 4, dt, dl)
+    assert torch.equal(out, want)
+    # Queries may be written over: the output in the query columns themselves.
+    same, _ = qkn.qknorm_kv4_attention(cache, q, 4, dt, dl, out=q[:, :256])
+    assert torch.equal(same, want)
+
+
 def test_attention_sharp_and_large_logits():
     """One row takes all the weight; logits far from zero; V scales far apart."""
     lens = [300, 300]
@@ -519,6 +558,30 @@ def test_captured_and_replayed():
         # An eager call on the graph's workspace.
         other = b.rows(1)
         qkn.qknorm_kv4_attention(a.cache, other, a.Hq, a.tables[0], a.lens, workspace=ws)
+
+
+def test_two_graphs_share_a_workspace():
+    """Captured calls of different sizes on one workspace, replayed in turn."""
+    a, b = Server(11), Server(12, prompt=50)
+    pa, pb = a.rows(50), b.rows(20)
+    a.step(pa, 50)
+    b.step(pb, 20)
+    xa, xb = a.rows(1), b.rows(1)
+    wide = torch.cat([b.tables[0], torch.full((3, 4000), -1, dtype=torch.int32, device="cuda")], 1)
+    ws = qkn.kv4_attention_workspace(b.cache, xb, b.Hq, wide, add_scores=True)
+    want_a = qkn.qknorm_kv4_attention(a.cache, xa, a.Hq, a.tables[0], a.lens)
+    want_b = qkn.qknorm_kv4_attention(b.cache, xb, b.Hq, wide, b.lens)
+    graphs, outs = [], []
+    for c, x, s, t in ((a.cache, xa, a, a.tables[0]), (b.cache, xb, b, wide)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(qkn.qknorm_kv4_attention(c, x, s.Hq, t, s.lens, add_scores=c is b.cache,
+                                                 workspace=ws))
+        graphs.append(g)
+    for _ in range(2):
+        for g, got, want in zip(graphs, outs, (want_a, want_b)):
+            g.replay()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_on_another_stream():
