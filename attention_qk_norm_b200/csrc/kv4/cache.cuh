@@ -89,6 +89,114 @@ __device__ __forceinline__ void unpack_params(uint32_t w, float &scale, float &m
 // ----------------------------------------------------------------- append --
 constexpr int kAppendThreads = 256;
 
+// ---- a row's sum of squares --
+// The squares, each rounded, are added in the order in which torch reduces a
+// contiguous fp32 row of D elements: D = 64 by halving (i and i + 32, then 16,
+// ...), D = 128 fours in element order and then the 32 sums by halving, D = 256
+// first i and i + 128.  A norm that differs in its last bit rounds a few
+// outputs the other way, and a key that differs by a rounding can be held a
+// whole code apart; in this order the append gives, bit for bit, what
+// elementary torch operations give.
+//
+// tree_sum: halving over kLanes lanes' N values each, the values' index below
+// the lanes'.  While a lane has more than one value, each step of the tree
+// sends one half of them and keeps the sums of the other, so that N values cost
+// little more than one; the halves then meet again, in the tree's order.
+// kHeld: the lanes' upper bit was halved before, and picks the value's class.
+template <int kLanes, int N, bool kHeld = false>
+__device__ __forceinline__ float tree_sum(float (&w)[N], int lane)
+{
+    int n = N;
+    int split[6] = {}, splits = 0;
+    if (kHeld) split[splits++] = kLanes / 2;
+#pragma unroll
+    for (int o = kHeld ? kLanes / 4 : kLanes / 2; o > 0; o /= 2) {
+        if (n > 1) {
+            n /= 2;
+            split[splits++] = o;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                if (i < n) {
+                    const bool up = lane & o;
+                    const float send = up ? w[i] : w[i + n];
+                    const float keep = up ? w[i + n] : w[i];
+                    w[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, o));
+                }
+        } else {
+            w[0] = __fadd_rn(w[0], __shfl_xor_sync(0xffffffffu, w[0], o));
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 6; ++k)
+        if (k < splits) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i < n) w[i] = __fadd_rn(w[i], __shfl_xor_sync(0xffffffffu, w[i], split[k]));
+        }
+#pragma unroll
+    for (int h = N / 2; h > 0; h /= 2)
+        if (h < n) {
+#pragma unroll
+            for (int i = 0; i < h; ++i) w[i] = __fadd_rn(w[i], w[i + h]);
+        }
+    return w[0];
+}
+// Sums of N elements in fours, each in element order.
+template <int N>
+__device__ __forceinline__ void fours(const float (&x)[N], float (&c)[N / 4])
+{
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+        c[i] = __fadd_rn(__fadd_rn(__fadd_rn(x[4 * i], x[4 * i + 1]), x[4 * i + 2]), x[4 * i + 3]);
+}
+// Lane l of kLanes holds vectors l and, with kVecs = 2, l + kLanes.
+template <int D, int kLanes, int kVecs, int kVec>
+__device__ __forceinline__ float square_sum(const float (&f)[kVecs][kVec], int lane)
+{
+    static_assert(kVecs <= 2, "two vectors to a lane");
+    float q[kVecs][kVec];
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) q[v][e] = __fmul_rn(f[v][e], f[v][e]);
+    if constexpr (D == 64 || (D == 256 && kVecs == 2)) {
+        // The two vectors are half a row apart.
+        if constexpr (kVecs == 2) {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) q[0][e] = __fadd_rn(q[0][e], q[1][e]);
+        }
+        if constexpr (D == 64) {
+            return tree_sum<kLanes, kVec>(q[0], lane);
+        } else {
+            float c[kVec / 4];
+            fours(q[0], c);
+            return tree_sum<kLanes, kVec / 4>(c, lane);
+        }
+    } else if constexpr (D == 128) {
+        float c[kVec / 4];
+        fours(q[0], c);
+        if constexpr (kVecs == 2) {
+            float c1[kVec / 4];
+            fours(q[1], c1);
+#pragma unroll
+            for (int i = 0; i < kVec / 4; ++i) c[i] = __fadd_rn(c[i], c1[i]);
+        }
+        return tree_sum<kLanes, kVec / 4>(c, lane);
+    } else {
+        // Half a row apart lies half the lanes away.
+        const bool up = lane & (kLanes / 2);
+        float x[kVec / 2], c[kVec / 8];
+#pragma unroll
+        for (int e = 0; e < kVec / 2; ++e) {
+            const float send = up ? q[0][e] : q[0][e + kVec / 2];
+            const float keep = up ? q[0][e + kVec / 2] : q[0][e];
+            x[e] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, kLanes / 2));
+        }
+        fours(x, c);
+        return tree_sum<kLanes, kVec / 8, true>(c, lane);
+    }
+}
+
 // One sub-warp holds a (token, head) row, as in the per-head QK-Norm kernel,
 // and visits rows with a grid stride, kU at a time in flight.  A row is read
 // once: its sum of squares, its extremes and its codes all come from the same
@@ -101,9 +209,7 @@ enum RowKind { kQueryRows, kKeyRows, kValueRows };
 
 // Lanes to a row: one 16-byte vector to a lane for query rows; for stored
 // rows, whose extremes, slot and parameters are work for each lane, two (FP8's
-// vectors are 16 elements: one).  (The sum of squares keeps the per-head
-// kernel's order either way: a lane's two vectors are the ones that its first
-// shuffle would have added.)
+// vectors are 16 elements: one).
 template <typename TS, int D, bool kStored>
 constexpr int kAppendLanes = D / Storage<TS>::kVec > 32  ? 32
                              : kStored && Storage<TS>::kVec <= 8 ? D / Storage<TS>::kVec / 2
@@ -125,8 +231,6 @@ __device__ __forceinline__ void append_rows(TS *__restrict__ qkv, int64_t row_st
     constexpr int kVPL = kNV / kLPR;
     constexpr int kEPL = kVPL * kVec;
     constexpr int kU = kAppendRows<TS, D, kKind != kQueryRows>;
-    constexpr bool kPairs = kVPL == 2 && kNV <= 32;  // the first shuffle's sum in the lane
-    constexpr bool kPacked = kVec == 16;  // the per-head kernel's order of sums
     constexpr bool kScale = kNorm && kKind != kValueRows;
 
     const uint64_t tid = (uint64_t)block * kAppendThreads + threadIdx.x;
@@ -177,21 +281,7 @@ __device__ __forceinline__ void append_rows(TS *__restrict__ qkv, int64_t row_st
 #pragma unroll
             for (int v = 0; v < kVPL; ++v) S::unpack(x[k][v], f[v]);
             if constexpr (kScale) {
-                float s = 0.f;
-#pragma unroll
-                for (int v = 0; v < kVPL; ++v) {
-                    float part = kPairs ? 0.f : s;
-                    if constexpr (kPacked) {
-                        uint64_t acc = f2_pack(0.f, 0.f);
-                        sumsq_acc(acc, f[v]);
-                        part = sumsq_total(acc);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < kVec; ++e) part = fmaf(f[v][e], f[v][e], part);
-                    }
-                    s = kPairs ? s + part : part;
-                }
-                rinv = rsqrtf(group_sum<kLPR>(s) / (float)D + eps);
+                rinv = rsqrtf(square_sum<D, kLPR, kVPL, kVec>(f, lane) / (float)D + eps);
 #pragma unroll
                 for (int v = 0; v < kVPL; ++v) {
                     float o[kVec];

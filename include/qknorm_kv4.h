@@ -60,9 +60,11 @@ extern "C" {
 #endif
 
 /*
- * Store new tokens: per-head QK-Norm of a fused QKV buffer in place (exactly
- * qknorm_per_head), with its key and value rows also written to the cache, in
- * one pass over the buffer.  Token t's rows go to slot slots[t] (int64, device,
+ * Store new tokens: per-head QK-Norm of a fused QKV buffer in place, with its
+ * key and value rows also written to the cache, in one pass over the buffer.
+ * The formula is qknorm_per_head's; the squares are added in the order in which
+ * torch reduces a row, so that a value may differ from qknorm_per_head's by one
+ * step of the type.  Token t's rows go to slot slots[t] (int64, device,
  * 8-byte aligned); a negative slot stores nothing (a padded token; its norm is
  * still done).  With gamma_q and gamma_k both NULL nothing is normalised and
  * only K and V are read: the buffer was normalised before, layerwise for
