@@ -97,8 +97,7 @@ class KV4Cache:
     for eviction, ``scores`` (float32 [num_pages, Hk, page_size]).  The tensors
     are the caller's; ``KV4Cache.empty`` allocates them, scores zeroed."""
 
-    __slots__ = ("pool", "scores", "Hk", "D", "page_size", "num_pages", "index", "_pool_ptr",
-                 "_scores_ptr")
+    __slots__ = ("pool", "scores", "Hk", "D", "page_size", "num_pages", "index")
 
     def __init__(self, pool, Hk, D, page_size=64, scores=None):
         _torch()
@@ -123,8 +122,6 @@ class KV4Cache:
         self.pool, self.scores = pool, scores
         self.Hk, self.D, self.page_size, self.num_pages = Hk, D, page_size, pages
         self.index = index
-        self._pool_ptr = pool.data_ptr()
-        self._scores_ptr = None if scores is None else scores.data_ptr()
 
     @classmethod
     def empty(cls, num_pages, Hk, D, page_size=64, scores=False, device="cuda"):
@@ -204,13 +201,16 @@ def qknorm_kv4_append(cache, qkv, slots, Hq, gamma_q=None, gamma_k=None, eps=1e-
     if stream is not None or _device_now() != index:
         with _Elsewhere(cache.pool.device, stream):
             return qknorm_kv4_append(cache, qkv, slots, Hq, gamma_q, gamma_k, eps)
-    T, _, stride = _rows(qkv, "qkv", index)
+    T, width, stride = _rows(qkv, "qkv", index)
     D = cache.D
+    if width < (Hq + 2 * cache.Hk) * D:
+        raise ValueError("qkv has fewer than (Hq + 2 * Hk) * D columns")
     rc = (_kv4_lib or _lib()).qknorm_kv4_append(
         qkv.data_ptr(), _code(qkv, "qkv"), T, Hq, cache.Hk, D, stride,
         _weights(gamma_q, "gamma_q", D, index), _weights(gamma_k, "gamma_k", D, index), eps,
-        _vec(slots, "slots", torch.int64, T, index), cache._pool_ptr, cache.num_pages,
-        cache.page_size, cache._scores_ptr, _raw_stream(index))
+        _vec(slots, "slots", torch.int64, T, index), cache.pool.data_ptr(), cache.num_pages,
+        cache.page_size, None if cache.scores is None else cache.scores.data_ptr(),
+        _raw_stream(index))
     if rc:
         _check("qknorm_kv4_append", rc)
     return qkv
@@ -228,8 +228,8 @@ def qknorm_kv4_read(cache, slots, dtype=None, stream=None):
     sp = _vec(slots, "slots", torch.int64, N, index)
     k, v = cache.pool.new_empty((2, N, width), dtype=dtype or torch.bfloat16).unbind(0)
     rc = (_kv4_lib or _lib()).qknorm_kv4_read(
-        cache._pool_ptr, cache.num_pages, cache.page_size, cache.Hk, cache.D, sp, N, k.data_ptr(),
-        v.data_ptr(), _code(k, "dtype"), width, _raw_stream(index))
+        cache.pool.data_ptr(), cache.num_pages, cache.page_size, cache.Hk, cache.D, sp, N,
+        k.data_ptr(), v.data_ptr(), _code(k, "dtype"), width, _raw_stream(index))
     if rc:
         _check("qknorm_kv4_read", rc)
     return k, v
@@ -296,10 +296,10 @@ def qknorm_kv4_attention(cache, qkv, Hq, page_table, kv_lens, q_starts=None, max
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on the cache's device")
     rc = (_kv4_lib or _lib()).qknorm_kv4_attention(
-        qkv.data_ptr(), code, T, Hq, cache.Hk, D, stride, cache._pool_ptr, cache.num_pages,
+        qkv.data_ptr(), code, T, Hq, cache.Hk, D, stride, cache.pool.data_ptr(), cache.num_pages,
         cache.page_size, tp, t_stride, pages, lp, B, qp, max_q,
         D ** -0.5 if scale is None else scale, out.data_ptr(), out_stride, lse.data_ptr(),
-        cache._scores_ptr if add_scores else None, workspace.data_ptr(), workspace.nbytes,
+        cache.scores.data_ptr() if add_scores else None, workspace.data_ptr(), workspace.nbytes,
         _raw_stream(index))
     if rc:
         _check("qknorm_kv4_attention", rc)
@@ -327,9 +327,9 @@ def qknorm_kv4_evict(cache, page_table, kv_lens, dst_table, budget, recent, stre
     new_lens = kv_lens.new_empty(B)
     kept = kv_lens.new_empty((B, cache.Hk, budget))
     rc = (_kv4_lib or _lib()).qknorm_kv4_evict(
-        cache._pool_ptr, cache.num_pages, cache.page_size, cache.Hk, cache.D, cache._scores_ptr,
-        tp, t_stride, pages, lp, B, dp, d_stride, d_pages, budget, recent, new_lens.data_ptr(),
-        kept.data_ptr(), _raw_stream(index))
+        cache.pool.data_ptr(), cache.num_pages, cache.page_size, cache.Hk, cache.D,
+        cache.scores.data_ptr(), tp, t_stride, pages, lp, B, dp, d_stride, d_pages, budget, recent,
+        new_lens.data_ptr(), kept.data_ptr(), _raw_stream(index))
     if rc:
         _check("qknorm_kv4_evict", rc)
     return new_lens, kept

@@ -1,5 +1,5 @@
 // attention.cuh -- attention over the 4-bit cache.
-// Part of libqknorm.so; included by kv4.cu.
+// Part of libqknorm.so; included by attention_*.cu and, for its plan, kv4.cu.
 //
 // The work is one pass over the cached rows: a row's D + 8 bytes meet a few
 // query rows (the group of query heads that share the key/value head, times
@@ -17,6 +17,8 @@
 // straight into operand registers, and nothing passes through shared memory
 // between the two products: S^T leaves the first with a cached row to a lane
 // group, the weights are transposed by movmatrix into the second's operand.
+// (Rows g and g + 8 of a 16-row operand are rows 2 g and 2 g + 1 of the block,
+// the order in which V's transposed bytes pair them.)
 // The codes are whole numbers, exact in fp16, and the row's scale and middle
 // come in on the 16x8 results:
 //     logit = scale_k * (q . (c - 8)) + mid_k * sum(q)
@@ -431,8 +433,6 @@ constexpr int kWeightExp = 6;
 constexpr float kLag = 8.f;
 constexpr float kLeastScale = 7.7037197e-34f;  // 2^-110
 
-// Tile rows g and g + 8 (and so columns of the second product) are the block's
-// rows 2 g and 2 g + 1, the order in which V's transposed bytes pair them.
 // Adds to add[v] the weights of `rows` query rows for the cached rows whose
 // logit records lie `stride` apart from x on (at[v] < 0: none); ml(r) is a
 // query row's maximum and 1 / sum.  A record is two logits, or fours of them.
@@ -506,7 +506,7 @@ __device__ __forceinline__ void add_scores(const AttentionArgs &a, int b, int hk
 
 // kWarps: kRunWarps, each block taking its run of the call's units; or more,
 // each block taking one whole item, for calls whose items are few and short
-// enough (see choose_warps): no lengths to add up, no parts to join.
+// enough (see launch_whole): no lengths to add up, no parts to join.
 template <typename TS, int D, int NT>
 constexpr int kRunBlocks = D == 256 || NT > 1 || sizeof(TS) == 4 ? 2 : 4;  // resident on an SM
 template <typename TS, int D, int NT, int kWarps>

@@ -253,12 +253,15 @@ int run_evict(const EvictArgs &a, cudaStream_t stream)
                        : launch_evict<D, false>(a, 1, rows, stream);
 }
 
+// Rows of a sequence at most: row numbers a little past the last fit 32 bits.
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
+
 int attention_shape(int64_t B, int dtype, int Hq, int Hk, int D, int max_q, int64_t max_kv)
 {
     if (elem_size(dtype) == 0) return QKN_ERR_UNSUPPORTED;
     if (D != 64 && D != 128 && D != 256) return QKN_ERR_UNSUPPORTED;
     if (B < 0 || B > 65535 || Hk < 1 || Hq < 1 || Hq > 65535 || Hq % Hk != 0 || max_q < 1 ||
-        max_q > 65535 || max_kv < 0 || max_kv > INT32_MAX)
+        max_q > 65535 || max_kv < 0 || max_kv > kMaxRows)
         return QKN_ERR_SHAPE;
     if ((int64_t)max_q * (Hq / Hk) > 1 << 30) return QKN_ERR_SHAPE;
     return QKN_OK;
@@ -324,7 +327,7 @@ int qknorm_kv4_attention(const void *q, int dtype, int64_t T, int Hq, int Hk, in
                          float scale, void *out, int64_t out_stride, float *lse, float *scores,
                          void *workspace, int64_t workspace_bytes, void *stream)
 {
-    if (page_size < 16 || page_size > 256 || max_pages < 0 || max_pages > INT32_MAX / page_size)
+    if (page_size < 16 || page_size > 256 || max_pages < 0 || max_pages > kMaxRows / page_size)
         return QKN_ERR_SHAPE;
     int rc = attention_shape(B, dtype, Hq, Hk, D, max_q, max_pages * page_size);
     if (rc != QKN_OK) return rc;
@@ -392,8 +395,8 @@ int qknorm_kv4_evict(void *pool, int64_t num_pages, int page_size, int Hk, int D
                      int32_t *new_lens, int32_t *kept, void *stream)
 {
     Pool p = {};
-    if (page_size < 16 || page_size > 256 || max_pages < 0 || max_pages > INT32_MAX / page_size ||
-        dst_pages < 0 || dst_pages > INT32_MAX / page_size)
+    if (page_size < 16 || page_size > 256 || max_pages < 0 || max_pages > kMaxRows / page_size ||
+        dst_pages < 0 || dst_pages > kMaxRows / page_size)
         return QKN_ERR_SHAPE;
     if (B < 0 || table_stride < max_pages || dst_stride < dst_pages || budget < 1 ||
         budget > dst_pages * page_size || recent < 0 || recent > budget || Hk < 1 ||

@@ -20,7 +20,7 @@
  * is slot s % page_size of page s / page_size.  `scores`, where a cache has
  * them, is float[num_pages][Hk][page_size]: each slot's accumulated attention
  * weight.  A sequence's rows 0, 1, 2, ... lie in the pages its row of the
- * page table names, page_size to a page.
+ * page table names, page_size to a page, at most 2^30 of them.
  *
  * How a row y[0..D) is held (fp32 arithmetic, each step rounded to nearest):
  *     s = (max/2 - min/2) * (2/15), 0 if below 2^-126;   m = min + 8*s
@@ -87,7 +87,8 @@ int qknorm_kv4_read(const void *pool, int64_t num_pages, int page_size, int Hk, 
                     int64_t row_stride, void *stream);
 
 /*
- * Attention over the cache.  B sequences; sequence b has kv_lens[b] cached
+ * Attention over the cache.  B sequences (B, Hq and max_q at most 65535);
+ * sequence b has kv_lens[b] cached
  * rows (int32) in the pages page_table[b * table_stride + 0 .. max_pages)
  * (int32) and the query tokens q_starts[b] .. q_starts[b+1] (int32, B + 1
  * entries, non-decreasing, at most max_q tokens each) of the fused buffer q

@@ -115,7 +115,8 @@ def test_attention_workspace(lib):
     assert w(3, BF16, 16, 2, 128, 1, 256, 1, n) == OK and n.value >= small
     # Enough is accepted (the call then meets the next check), one byte less is not.
     assert attention(lib, wsb=small - 1) == SHAPE
-    assert w(65535, FP32, 128, 8, 256, 65535, 2 ** 31 - 256, 1, n) == OK and n.value > 0
+    assert w(65535, FP32, 128, 8, 256, 65535, 2 ** 30, 1, n) == OK and n.value > 0
+    assert w(1, FP32, 128, 8, 256, 1, 2 ** 30 + 1, 1, n) == SHAPE
     # More rows or units than 32-bit numbers hold: refused before anything is touched.
     assert w(1, BF16, 65535, 1, 64, 65535, 256, 0, n) == SHAPE
     big = dict(B=60000, T=60000, maxp=1 << 20, tstride=1 << 20, wsb=2 ** 62)
@@ -131,7 +132,8 @@ def test_evict_validation(lib):
     assert f(D=32) == UNSUP
     for bad in (dict(budget=0), dict(budget=129), dict(recent=-1), dict(recent=101), dict(B=-1),
                 dict(tstride=3), dict(dstride=1), dict(dpages=1), dict(page=33), dict(pages=0),
-                dict(Hk=0), dict(maxp=-1), dict(dpages=-1), dict(B=1 << 31)):
+                dict(Hk=0), dict(maxp=-1), dict(dpages=-1), dict(B=1 << 31),
+                dict(maxp=(1 << 24) + 1, tstride=1 << 25)):
         assert f(**bad) == SHAPE, bad
     for bad in (dict(pool=None), dict(scores=None), dict(table=None), dict(lens=None),
                 dict(dst=None), dict(new=None), dict(kept=None)):

@@ -639,6 +639,7 @@ def test_binding_refusals():
                                           s.Hq),
             lambda: qkn.qknorm_kv4_append(c, x, torch.zeros(3, dtype=torch.int64, device="cuda"),
                                           s.Hq, s.gq[:64], s.gk),
+            lambda: qkn.qknorm_kv4_append(c, x[:, :256], s.slots(1), s.Hq),
             lambda: qkn.qknorm_kv4_read(c, torch.zeros(3, dtype=torch.int32, device="cuda"))):
         with pytest.raises((ValueError, TypeError)):
             call()
