@@ -373,10 +373,7 @@ qkn_kv4_append_kernel(TS *__restrict__ qkv, int64_t row_stride, int64_t T, int H
 // to a lane (four in fp32 at D = 256): a row's slot, page and parameters are
 // work for each lane, and one vector to a lane was bound by it.
 template <typename TS, int D>
-constexpr int kReadLanes = D / Storage<TS>::kVec < 4 ? D / Storage<TS>::kVec
-                                                     : (D / Storage<TS>::kVec >= 64
-                                                            ? 16
-                                                            : D / Storage<TS>::kVec / 2);
+constexpr int kReadLanes = D / Storage<TS>::kVec >= 64 ? 16 : D / Storage<TS>::kVec / 2;
 template <typename TS, int D>
 __global__ void __launch_bounds__(kAppendThreads)
 qkn_kv4_read_kernel(const Pool pool, const int64_t *__restrict__ slots, int64_t N,

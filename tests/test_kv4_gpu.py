@@ -609,6 +609,28 @@ def test_on_another_stream():
         assert torch.equal(out, want) and torch.equal(lse, wlse)
 
 
+def test_two_calls_at_once():
+    """Split calls on two streams, each with a workspace of its own."""
+    lens = [9000, 41, 7000]
+    dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    calls = []
+    for seed in (21, 22):
+        cache, q, table, _ = problem(seed, lens, [1] * 3, 8, 2, 128, 64, "bf16", True)
+        want = qkn.qknorm_kv4_attention(cache, q, 8, table.cuda(), dl, add_scores=True)
+        calls.append((cache, q, table.cuda(), want, cache.scores.clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for cache, q, table, _, _, stream in calls:
+            cache.scores.zero_()
+            stream.wait_stream(torch.cuda.current_stream())
+            got.append(qkn.qknorm_kv4_attention(cache, q, 8, table, dl, add_scores=True,
+                                                stream=stream))
+        torch.cuda.synchronize()
+        for (o, l), (cache, _, _, (wo, wl), sums, _) in zip(got, calls):
+            assert torch.equal(o, wo) and torch.equal(l, wl) and torch.equal(cache.scores, sums)
+
+
 def test_binding_refusals():
     s = Server(6)
     x = s.rows(1)
